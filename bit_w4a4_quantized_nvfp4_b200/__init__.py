@@ -1,4 +1,5 @@
-"""B200 (sm_100a) SVDQuant W4A4 and AWQ W4A16 linear layers.
+"""B200 (sm_100a) SVDQuant W4A4 and AWQ W4A16 linear layers, with the 8-bit
+(E4M3) linear layer and the rotary positions that stand beside them.
 
 A thin ctypes binding over ``libsvdq.so`` (C ABI in ``include/svdq.h``).
 Every function here only marshals arguments: torch tensors provide device
@@ -19,6 +20,7 @@ from __future__ import annotations
 
 import ctypes as C
 import enum
+import math
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -28,12 +30,15 @@ import torch
 __all__ = [
     "NVFP4", "INT4", "Status", "SvdqError", "PackedWeight", "QuantAct", "AwqWeight",
     "library_path", "load", "scale_bytes", "pack_weight", "quantize_act", "w4a4_linear",
-    "w4a4_linear_qkv", "qkv_norm_rope", "RopeTable", "pack_rope", "svdq_linear", "awq_pack_weight", "awq_w4a16_linear", "device_error", "set_wait_limit_ns",
+    "w4a4_linear_qkv", "qkv_norm_rope", "RopeTable", "pack_rope", "svdq_linear", "awq_pack_weight", "awq_w4a16_linear",
+    "Fp8Act", "Fp8Weight", "fp8_quantize_act", "fp8_norm_quantize", "fp8_pack_weight", "fp8_linear",
+    "RopeFreqs", "rope_freqs", "rope_tables", "rope_apply", "device_error", "set_wait_limit_ns",
     "probe_convert", "probe_wait_timeout", "probe_mma_peak", "debug_force_arch",
 ]
 
 NVFP4, INT4 = 0, 1
 _OUT = {"bf16": 0, "f32": 1, "i32_groups": 2, "bf16_gelu": 3}
+_ROPE_LAYOUT = {"interleaved": 0, "half": 1}
 _HERE = os.path.dirname(os.path.abspath(__file__))
 
 
@@ -75,6 +80,12 @@ SIGNATURES = {
     "svdq_qkv_norm_rope": (_I, [_I, _I, _P, _P, _F, _P, _P, _P, _P]),
     "awq_pack_weight": (_I, [_I, _I, _P, _P, _P, _P, _P]),
     "awq_w4a16_linear": (_I, [_I, _I, _I, _P, _P, _P, _P, _P, _P, _P]),
+    "svdq_fp8_quantize_act": (_I, [_I, _I, _P, _I64, _P, _P, _P]),
+    "svdq_fp8_norm_quantize": (_I, [_I, _I, _P, _I64, _P, _I64, _P, _F, _P, _I64, _P, _P, _P]),
+    "svdq_fp8_pack_weight": (_I, [_I, _I, _P, _P, _P, _P]),
+    "svdq_fp8_linear": (_I, [_I, _I, _I, _P, _P, _P, _P, _P, _P, _I, _P]),
+    "svdq_rope_tables": (_I, [_I, _I, _I, _P, _P, _P, _F, _P, _P, _P]),
+    "svdq_rope_apply": (_I, [_I, _I, _I, _I, _I, _I, _P, _P, _P, _F, _P, _I64, _P, _I64, _P]),
     "svdq_device_error": (_I, [_P]),
     "svdq_set_wait_limit_ns": (None, [_U64]),
     "svdq_probe_convert": (_I, [_P, _I64, _P, _P, _P, _P]),
@@ -421,6 +432,274 @@ def awq_w4a16_linear(x: torch.Tensor, w: AwqWeight, bias: Optional[torch.Tensor]
     _check("awq_w4a16_linear", load().awq_w4a16_linear(
         M, K, w.N, _ptr(x), _ptr(w.q), _ptr(w.scales), _ptr(w.zeros), _ptr(bias), _ptr(out),
         _stream(stream)))
+    return out
+
+
+# ------------------------------------------------------------------ the 8-bit linear layer
+@dataclass
+class Fp8Act:
+    """bf16 activations in 8 bits: E4M3 codes and one fp32 scale per 128 columns of a row."""
+    M: int
+    K: int
+    codes: torch.Tensor   # float8_e4m3fn [M, K]
+    scales: torch.Tensor  # float32 [ceil(K/128), M]
+
+
+@dataclass
+class Fp8Weight:
+    """A weight in 8 bits: E4M3 codes and one fp32 scale per 128 x 128 block."""
+    K: int
+    N: int
+    codes: torch.Tensor   # float8_e4m3fn [N, K]
+    scales: torch.Tensor  # float32 [ceil(N/128), ceil(K/128)]
+
+
+_F8 = torch.float8_e4m3fn
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _rows(t: torch.Tensor, name: str, cols: Optional[int] = None) -> int:
+    """Row stride (elements) of a bf16 [M, K] tensor whose rows may be a
+    column range of a wider tensor: unit column stride, and rows that follow
+    one another without overlap (a stride in a dimension of size one says
+    nothing and is not looked at)."""
+    if t.dtype is not torch.bfloat16 or t.dim() != 2:
+        raise ValueError(f"{name}: expected bfloat16 [M, K]")
+    M, K = t.shape
+    if cols is not None and K != cols:
+        raise ValueError(f"{name}: {K} columns, expected {cols}")
+    s0, s1 = t.stride()
+    if K > 1 and s1 != 1:
+        raise ValueError(f"{name}: expected unit stride along the columns")
+    if M <= 1:
+        return (K + 7) // 8 * 8
+    if s0 < K:
+        raise ValueError(f"{name}: row stride {s0} is less than the row's {K} columns")
+    return s0
+
+
+def _addr(t: torch.Tensor, dev: int, name: str) -> int:
+    """Device address of a CUDA tensor of any strides on device ``dev``."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: tensor on {t.device}, but the current device is cuda:{dev}")
+    return t.data_ptr()
+
+
+def _current(t: torch.Tensor) -> int:
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    return torch.cuda.current_device()
+
+
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """An output of a call on ``stream``: allocated for the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _fp8_act_out(out: Optional[Fp8Act], M: int, K: int, device, stream) -> Fp8Act:
+    if out is None:
+        return Fp8Act(M, K, _new((M, K), _F8, device, stream), _new((_blocks(K), M), torch.float32, device, stream))
+    _need(out.M == M and out.K == K, "out: Fp8Act of M {}, K {}", out.M, out.K)
+    _is(out.codes, _F8, (M, K), "out.codes")
+    _is(out.scales, torch.float32, (_blocks(K), M), "out.scales")
+    return out
+
+
+def fp8_quantize_act(x: torch.Tensor, stream=None, out: Optional[Fp8Act] = None) -> Fp8Act:
+    """svdq_fp8_quantize_act: x bf16 [M, K] (rows may be strided) -> codes, scales."""
+    ldx = _rows(x, "x")
+    M, K = x.shape
+    dev = _current(x)
+    out = _fp8_act_out(out, M, K, x.device, stream)
+    _check("svdq_fp8_quantize_act", load().svdq_fp8_quantize_act(
+        M, K, _addr(x, dev, "x"), ldx, _ptr(out.codes, dev), _ptr(out.scales, dev), _stream(stream)))
+    return out
+
+
+def fp8_norm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
+                      stream=None, out: Optional[Fp8Act] = None, residual_out: Optional[torch.Tensor] = None):
+    """svdq_fp8_norm_quantize: r = bf16(x + residual), then the 8-bit form of
+    RMSNorm(r) * weight. Returns (Fp8Act, r); r is None without a residual.
+    x, residual and residual_out bf16 [M, K], rows may be strided;
+    residual_out may be x or residual (in place)."""
+    ldx = _rows(x, "x")
+    M, K = x.shape
+    _is(weight, torch.bfloat16, (K,), "weight")
+    dev = _current(x)
+    ldr = ldo = 0
+    if residual is not None:
+        _need(residual.shape == x.shape, "residual: shape {}, x {}", tuple(residual.shape), tuple(x.shape))
+        ldr = _rows(residual, "residual")
+        if residual_out is None:
+            residual_out = _new((M, K), torch.bfloat16, x.device, stream)
+        _need(residual_out.shape == x.shape, "residual_out: shape {}, x {}", tuple(residual_out.shape),
+              tuple(x.shape))
+        ldo = _rows(residual_out, "residual_out")
+    else:
+        _need(residual_out is None, "residual_out given without residual")
+    out = _fp8_act_out(out, M, K, x.device, stream)
+    _check("svdq_fp8_norm_quantize", load().svdq_fp8_norm_quantize(
+        M, K, _addr(x, dev, "x"), ldx, None if residual is None else _addr(residual, dev, "residual"), ldr,
+        _ptr(weight, dev), float(eps), None if residual is None else _addr(residual_out, dev, "residual_out"), ldo,
+        _ptr(out.codes, dev), _ptr(out.scales, dev), _stream(stream)))
+    return out, residual_out
+
+
+def fp8_pack_weight(W: torch.Tensor, stream=None, out: Optional[Fp8Weight] = None) -> Fp8Weight:
+    """svdq_fp8_pack_weight: W fp32 [K, N] -> codes, scales (into ``out``'s buffers when given)."""
+    _need(W.dim() == 2 and W.dtype == torch.float32, "W: expected float32 [K, N]")
+    K, N = W.shape
+    dev = _current(W)
+    if out is None:
+        out = Fp8Weight(K, N, _new((N, K), _F8, W.device, stream),
+                        _new((_blocks(N), _blocks(K)), torch.float32, W.device, stream))
+    else:
+        _need(out.K == K and out.N == N, "out: Fp8Weight of K {}, N {}", out.K, out.N)
+        _is(out.codes, _F8, (N, K), "out.codes")
+        _is(out.scales, torch.float32, (_blocks(N), _blocks(K)), "out.scales")
+    _check("svdq_fp8_pack_weight", load().svdq_fp8_pack_weight(
+        K, N, _ptr(W, dev), _ptr(out.codes, dev), _ptr(out.scales, dev), _stream(stream)))
+    return out
+
+
+def fp8_linear(qa: Fp8Act, w: Fp8Weight, bias: Optional[torch.Tensor] = None, out_dtype: str = "bf16", stream=None,
+               out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """svdq_fp8_linear: y [M, N] = the product of the 8-bit operands, + bias. out_dtype "bf16" or "f32"."""
+    M, K, N = qa.M, qa.K, w.N
+    _need(K == w.K, "activations have K = {}, the packed weight K = {}", K, w.K)
+    _need(out_dtype == "bf16" or out_dtype == "f32", "out_dtype {!r}", out_dtype)
+    G = _blocks(K)
+    _is(qa.codes, _F8, (M, K), "qa.codes")
+    _is(qa.scales, torch.float32, (G, M), "qa.scales")
+    _is(w.codes, _F8, (N, K), "w.codes")
+    _is(w.scales, torch.float32, (_blocks(N), G), "w.scales")
+    if bias is not None:
+        _is(bias, torch.bfloat16, (N,), "bias")
+    want = torch.bfloat16 if out_dtype == "bf16" else torch.float32
+    dev = _current(qa.codes)
+    if out is None:
+        out = _new((M, N), want, qa.codes.device, stream)
+    else:
+        _is(out, want, (M, N), "out")
+    _check("svdq_fp8_linear", load().svdq_fp8_linear(
+        M, K, N, _ptr(qa.codes, dev), _ptr(qa.scales, dev), _ptr(w.codes, dev), _ptr(w.scales, dev),
+        _ptr(bias, dev), _ptr(out, dev), _OUT[out_dtype], _stream(stream)))
+    return out
+
+
+# ------------------------------------------------------------------ rotary positions
+@dataclass
+class RopeFreqs:
+    """How rotary pairs turn: freq float64 [pairs], radians per position; the
+    factor on cos and sin; axis int32 [pairs], the position axis of each pair
+    (None: all pairs follow axis 0). Made once per model (rope_freqs)."""
+    freq: torch.Tensor
+    factor: float = 1.0
+    axis: Optional[torch.Tensor] = None
+
+
+def rope_freqs(rot_dim, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+               original_len: int = 0, device="cuda") -> RopeFreqs:
+    """The frequencies of heads whose first ``rot_dim`` columns turn: base **
+    (-2 i / rot_dim) for pair i, in 64 bits. rot_dim: an even number, or one
+    per position axis (their pairs follow one another).
+
+    scaling for contexts ``factor`` times longer than the trained one:
+      None      none
+      "linear"  every frequency divided by the factor
+      "ntk"     a larger base, with which the slowest pair slows by the factor
+                and the fastest keeps its frequency
+      "yarn"    pairs that turn less than once within original_len slow by the
+                factor, those that turn more than 32 times stay, a linear ramp
+                over the pair index between them; cos and sin times
+                0.1 ln(factor) + 1
+    """
+    dims = [int(rot_dim)] if isinstance(rot_dim, int) else [int(d) for d in rot_dim]
+    _need(1 <= len(dims) <= 8 and all(d >= 2 and d % 2 == 0 for d in dims), "rot_dim {!r}: even numbers expected",
+          rot_dim)
+    _need(scaling in (None, "linear", "ntk", "yarn"), "scaling {!r}", scaling)
+    _need(base > 1.0 and factor >= 1.0 and math.isfinite(base) and math.isfinite(factor), "base {}, factor {}",
+          base, factor)
+    _need(scaling != "yarn" or original_len > 0, "yarn needs original_len")
+    parts, mult = [], 1.0
+    for d in dims:
+        i = torch.arange(d // 2, dtype=torch.float64)
+        b = base * factor ** (d / (d - 2)) if scaling == "ntk" and d > 2 else base
+        f = b ** (-2.0 * i / d)
+        if scaling == "linear":
+            f = f / factor
+        elif scaling == "yarn":
+            # the (real-valued) pair index at which a pair turns `turns` times within original_len
+            def pair(turns):
+                return d * math.log(original_len / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+            lo, hi = max(math.floor(pair(32.0)), 0), min(math.ceil(pair(1.0)), d - 1)
+            slow = ((i - lo) / max(hi - lo, 0.001)).clamp(0.0, 1.0)
+            f = f / factor * slow + f * (1.0 - slow)
+            mult = 0.1 * math.log(factor) + 1.0
+        parts.append(f)
+    axis = None
+    if len(dims) > 1:
+        axis = torch.repeat_interleave(torch.arange(len(dims), dtype=torch.int32), torch.tensor(dims) // 2).to(device)
+    return RopeFreqs(torch.cat(parts).to(device), mult, axis)
+
+
+def _rope_inputs(positions: torch.Tensor, freqs: RopeFreqs, dev: int):
+    """(M, axes, pairs, pos, freq, axis) of a rotary call, checked."""
+    if positions.dtype is not torch.int64 or positions.dim() not in (1, 2):
+        raise ValueError("positions: expected int64 [M] or [M, axes]")
+    M, axes = positions.shape[0], 1 if positions.dim() == 1 else positions.shape[1]
+    f = freqs.freq
+    if f.dtype is not torch.float64 or f.dim() != 1:
+        raise ValueError("freqs.freq: expected float64 [pairs]")
+    pairs = f.shape[0]
+    if freqs.axis is not None:
+        _is(freqs.axis, torch.int32, (pairs,), "freqs.axis")
+    return M, axes, pairs, _ptr(positions, dev), _ptr(f, dev), _ptr(freqs.axis, dev)
+
+
+def rope_tables(positions: torch.Tensor, freqs: RopeFreqs, stream=None):
+    """svdq_rope_tables: (cos, sin) fp32 [M, pairs] at positions int64 [M] or
+    [M, axes], the tables that pack_rope (pairs = 64) and qkv_norm_rope take."""
+    dev = _current(positions)
+    M, axes, pairs, pp, pf, pa = _rope_inputs(positions, freqs, dev)
+    cos = _new((M, pairs), torch.float32, positions.device, stream)
+    sin = _new((M, pairs), torch.float32, positions.device, stream)
+    _check("svdq_rope_tables", load().svdq_rope_tables(M, axes, pairs, pp, pf, pa, float(freqs.factor),
+                                                       _ptr(cos, dev), _ptr(sin, dev), _stream(stream)))
+    return cos, sin
+
+
+def rope_apply(x: torch.Tensor, heads: int, head_dim: int, positions: torch.Tensor, freqs: RopeFreqs,
+               layout: str = "interleaved", stream=None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """svdq_rope_apply: rotates the first 2 * pairs columns of each of the
+    first ``heads`` heads of x bf16 [M, >= heads * head_dim] (rows may be
+    strided: x may be a whole Q/K/V projection, whose Q and K heads come
+    first). In place unless ``out`` [M, heads * head_dim] is given; returns
+    what was written to."""
+    _need(layout in _ROPE_LAYOUT, "layout {!r}", layout)
+    ldx = _rows(x, "x")
+    width = heads * head_dim
+    _need(heads >= 1 and head_dim >= 1 and x.shape[1] >= width, "x has {} columns, {} heads of {} need {}",
+          x.shape[1], heads, head_dim, width)
+    dev = _current(x)
+    M, axes, pairs, pp, pf, pa = _rope_inputs(positions, freqs, dev)
+    _need(M == x.shape[0], "positions: {} rows, x has {}", M, x.shape[0])
+    if out is None:
+        out, ldy = x, ldx
+    else:
+        ldy = _rows(out, "out", width)
+        _need(out.shape[0] == M, "out: {} rows, x has {}", out.shape[0], M)
+    _check("svdq_rope_apply", load().svdq_rope_apply(
+        M, heads, head_dim, pairs, _ROPE_LAYOUT[layout], axes, pp, pf, pa, float(freqs.factor), _addr(x, dev, "x"),
+        ldx, _addr(out, dev, "out"), ldy, _stream(stream)))
     return out
 
 

@@ -62,6 +62,37 @@ svdq_status check_common(svdq_precision p, int K, int r) {
   return SVDQ_OK;
 }
 
+bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Address ranges, for the refusal of outputs that overlap inputs.
+struct Span {
+  uintptr_t lo, hi;
+};
+Span span(const void* p, size_t bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return Span{a, a + bytes};
+}
+// `rows` rows of `cols` elements at row stride `ld`
+Span rows_span(const void* p, int rows, long long cols, long long ld, size_t elem) {
+  return span(p, ((size_t)(rows - 1) * (size_t)ld + (size_t)cols) * elem);
+}
+bool overlap(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
+Span fp8_scale_span(const float* scales, int M, int K) {
+  return span(scales, (size_t)((K + 127) / 128) * (size_t)M * sizeof(float));
+}
+bool rope_inputs_overlap(const Span& out, int M, int axes, int pairs, const long long* pos, const double* freq,
+                         const int* axis) {
+  return overlap(out, span(pos, (size_t)M * axes * 8)) || overlap(out, span(freq, (size_t)pairs * 8)) ||
+         (axis && overlap(out, span(axis, (size_t)pairs * 4)));
+}
+
+// Sizes of an 8-bit activation call: M rows of K columns at row stride ld.
+svdq_status check_fp8_act(int M, int K, long long ld) {
+  if (M < 0 || K <= 0) return SVDQ_ERR_INVALID_ARG;
+  if (K % 16 || ld < K || ld % 8) return SVDQ_ERR_SHAPE;
+  return SVDQ_OK;
+}
+
 }  // namespace
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -395,6 +426,126 @@ svdq_status awq_w4a16_linear(int M, int K, int N, const uint16_t* x, const uint8
   if (st != SVDQ_OK) return st;
   AwqArgs a{x, q, scales, zeros, bias, y, M, K, N};
   return from_cuda(launch_awq(a, err, g_wait_ns.load(), static_cast<cudaStream_t>(stream)));
+}
+
+svdq_status svdq_fp8_quantize_act(int M, int K, const uint16_t* x, long long ldx, uint8_t* codes, float* scales,
+                                  void* stream) {
+  svdq_status st = check_fp8_act(M, K, ldx);
+  if (st != SVDQ_OK || M == 0) return st;
+  if (!x || !codes || !scales) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return SVDQ_ERR_ALIGN;
+  const Span sx = rows_span(x, M, K, ldx, 2), sc = span(codes, (size_t)M * K), ss = fp8_scale_span(scales, M, K);
+  if (overlap(sc, sx) || overlap(ss, sx) || overlap(sc, ss)) return SVDQ_ERR_INVALID_ARG;
+  if ((st = device_info(nullptr, nullptr)) != SVDQ_OK) return st;
+  Fp8ActArgs a{x, nullptr, nullptr, nullptr, codes, scales, ldx, 0, 0, M, K, 0.f};
+  return from_cuda(launch_fp8_act(a, static_cast<cudaStream_t>(stream)));
+}
+
+svdq_status svdq_fp8_norm_quantize(int M, int K, const uint16_t* x, long long ldx, const uint16_t* residual,
+                                   long long ldr, const uint16_t* weight, float eps, uint16_t* residual_out,
+                                   long long ldo, uint8_t* codes, float* scales, void* stream) {
+  svdq_status st = check_fp8_act(M, K, ldx);
+  if (st != SVDQ_OK) return st;
+  if (K > kFp8NormMaxK) return SVDQ_ERR_SHAPE;
+  if (!(eps >= 0.0f && eps < 3.0e38f)) return SVDQ_ERR_INVALID_ARG;
+  if (M == 0) return SVDQ_OK;
+  if (!x || !weight || !codes || !scales) return SVDQ_ERR_INVALID_ARG;
+  if ((residual == nullptr) != (residual_out == nullptr)) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(weight) || !aligned16(codes) || !aligned16(scales) || !aligned16(residual) ||
+      !aligned16(residual_out))
+    return SVDQ_ERR_ALIGN;
+  const Span sx = rows_span(x, M, K, ldx, 2), sw = span(weight, (size_t)K * 2), sc = span(codes, (size_t)M * K),
+             ss = fp8_scale_span(scales, M, K);
+  if (overlap(sc, sx) || overlap(sc, sw) || overlap(ss, sx) || overlap(ss, sw) || overlap(sc, ss))
+    return SVDQ_ERR_INVALID_ARG;
+  if (residual) {
+    if (check_fp8_act(M, K, ldr) != SVDQ_OK || check_fp8_act(M, K, ldo) != SVDQ_OK) return SVDQ_ERR_SHAPE;
+    const Span sr = rows_span(residual, M, K, ldr, 2), so = rows_span(residual_out, M, K, ldo, 2);
+    if (overlap(sc, sr) || overlap(ss, sr) || overlap(so, sc) || overlap(so, ss) || overlap(so, sw))
+      return SVDQ_ERR_INVALID_ARG;
+    if (overlap(so, sx) && !(residual_out == x && ldo == ldx)) return SVDQ_ERR_INVALID_ARG;
+    if (overlap(so, sr) && !(residual_out == residual && ldo == ldr)) return SVDQ_ERR_INVALID_ARG;
+  }
+  if ((st = device_info(nullptr, nullptr)) != SVDQ_OK) return st;
+  Fp8ActArgs a{x, residual, weight, residual_out, codes, scales, ldx, ldr, ldo, M, K, eps};
+  return from_cuda(launch_fp8_act(a, static_cast<cudaStream_t>(stream)));
+}
+
+svdq_status svdq_fp8_pack_weight(int K, int N, const float* W, uint8_t* codes, float* scales, void* stream) {
+  if (K <= 0 || N <= 0) return SVDQ_ERR_INVALID_ARG;
+  if (K % 16 || N % 8) return SVDQ_ERR_SHAPE;
+  if (!W || !codes || !scales) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned16(W) || !aligned16(codes) || !aligned16(scales)) return SVDQ_ERR_ALIGN;
+  svdq_status st = device_info(nullptr, nullptr);
+  if (st != SVDQ_OK) return st;
+  return from_cuda(launch_fp8_pack(K, N, W, codes, scales, static_cast<cudaStream_t>(stream)));
+}
+
+svdq_status svdq_fp8_linear(int M, int K, int N, const uint8_t* x_codes, const float* x_scales,
+                            const uint8_t* w_codes, const float* w_scales, const uint16_t* bias, void* y,
+                            svdq_out_dtype out, void* stream) {
+  if (M < 0 || K <= 0 || N <= 0) return SVDQ_ERR_INVALID_ARG;
+  if (K % 16 || N % 8) return SVDQ_ERR_SHAPE;
+  if (out != SVDQ_OUT_BF16 && out != SVDQ_OUT_F32) return SVDQ_ERR_INVALID_ARG;
+  if (M == 0) return SVDQ_OK;
+  if (!x_codes || !x_scales || !w_codes || !w_scales || !y) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned16(x_codes) || !aligned16(w_codes) || !aligned16(y) || !aligned_to(x_scales, 4) ||
+      !aligned_to(w_scales, 4) || !aligned_to(bias, 4))
+    return SVDQ_ERR_ALIGN;
+  const size_t G = (size_t)(K + 127) / 128;
+  const Span sy = span(y, (size_t)M * N * (out == SVDQ_OUT_F32 ? 4 : 2));
+  if (overlap(sy, span(x_codes, (size_t)M * K)) || overlap(sy, fp8_scale_span(x_scales, M, K)) ||
+      overlap(sy, span(w_codes, (size_t)N * K)) || overlap(sy, span(w_scales, (size_t)(N + 127) / 128 * G * 4)) ||
+      (bias && overlap(sy, span(bias, (size_t)N * 2))))
+    return SVDQ_ERR_INVALID_ARG;
+  unsigned* err = nullptr;
+  int sms = 0;
+  svdq_status st = device_info(&err, &sms);
+  if (st != SVDQ_OK) return st;
+  Fp8GemmArgs a{x_codes, x_scales, w_codes, w_scales, bias, y, M, K, N, out == SVDQ_OUT_F32 ? 1 : 0, err,
+                g_wait_ns.load(), sms};
+  return from_cuda(launch_fp8_linear(a, static_cast<cudaStream_t>(stream)));
+}
+
+svdq_status svdq_rope_tables(int M, int axes, int pairs, const long long* pos, const double* freq, const int* axis,
+                             float factor, float* cos_t, float* sin_t, void* stream) {
+  if (M < 0 || axes < 1 || axes > 8 || pairs < 1) return SVDQ_ERR_INVALID_ARG;
+  if (pairs > kRopeMaxPairs) return SVDQ_ERR_SHAPE;
+  if (M == 0) return SVDQ_OK;
+  if (!pos || !freq || !cos_t || !sin_t) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned_to(pos, 8) || !aligned_to(freq, 8) || !aligned_to(axis, 4) || !aligned_to(cos_t, 4) ||
+      !aligned_to(sin_t, 4))
+    return SVDQ_ERR_ALIGN;
+  const Span c = span(cos_t, (size_t)M * pairs * 4), n = span(sin_t, (size_t)M * pairs * 4);
+  if (overlap(c, n) || rope_inputs_overlap(c, M, axes, pairs, pos, freq, axis) ||
+      rope_inputs_overlap(n, M, axes, pairs, pos, freq, axis))
+    return SVDQ_ERR_INVALID_ARG;
+  svdq_status st = device_info(nullptr, nullptr);
+  if (st != SVDQ_OK) return st;
+  RopeArgs a{pos, freq, axis, nullptr, nullptr, 0, 0, M, axes, pairs, 0, 0, 0, factor};
+  return from_cuda(launch_rope_tables(a, cos_t, sin_t, static_cast<cudaStream_t>(stream)));
+}
+
+svdq_status svdq_rope_apply(int M, int heads, int head_dim, int pairs, svdq_rope_layout layout, int axes,
+                            const long long* pos, const double* freq, const int* axis, float factor,
+                            const uint16_t* x, long long ldx, uint16_t* y, long long ldy, void* stream) {
+  if (M < 0 || heads < 1 || head_dim < 1 || axes < 1 || axes > 8 || pairs < 1) return SVDQ_ERR_INVALID_ARG;
+  if (layout != SVDQ_ROPE_INTERLEAVED && layout != SVDQ_ROPE_HALF) return SVDQ_ERR_INVALID_ARG;
+  if (pairs > kRopeMaxPairs || 2 * pairs > head_dim || head_dim % 8) return SVDQ_ERR_SHAPE;
+  const long long width = (long long)heads * head_dim;
+  if (width > (1 << 20) || ldx < width || ldy < width || ldx % 8 || ldy % 8) return SVDQ_ERR_SHAPE;
+  if (M == 0) return SVDQ_OK;
+  if (!pos || !freq || !x || !y) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(y) || !aligned_to(pos, 8) || !aligned_to(freq, 8) || !aligned_to(axis, 4))
+    return SVDQ_ERR_ALIGN;
+  const Span sx = rows_span(x, M, width, ldx, 2), sy = rows_span(y, M, width, ldy, 2);
+  if (overlap(sx, sy) && !(x == y && ldx == ldy)) return SVDQ_ERR_INVALID_ARG;
+  if (rope_inputs_overlap(sy, M, axes, pairs, pos, freq, axis)) return SVDQ_ERR_INVALID_ARG;
+  svdq_status st = device_info(nullptr, nullptr);
+  if (st != SVDQ_OK) return st;
+  RopeArgs a{pos, freq, axis, x, y, ldx, ldy, M, axes, pairs, heads, head_dim, layout == SVDQ_ROPE_HALF ? 1 : 0,
+             factor};
+  return from_cuda(launch_rope_apply(a, static_cast<cudaStream_t>(stream)));
 }
 
 svdq_status svdq_device_error(unsigned* bits) {

@@ -104,6 +104,52 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t s);
 // cos/sin [M, 64] -> the packed rotary table (16384 * ceil(M / 32) bytes)
 cudaError_t launch_rope_pack(int M, const float* cos_t, const float* sin_t, float* rope, cudaStream_t s);
 
+struct Fp8ActArgs {
+  const uint16_t* x;          // bf16 [M, K], row stride ldx
+  const uint16_t* residual;   // bf16 [M, K], row stride ldr, or null
+  const uint16_t* weight;     // bf16 [K] (norm) or null (no norm)
+  uint16_t* residual_out;     // bf16 [M, K], row stride ldo (with residual)
+  uint8_t* codes;             // [M, K]
+  float* scales;              // [ceil(K/128), M]
+  long long ldx, ldr, ldo;
+  int M, K;
+  float eps;
+};
+constexpr int kFp8NormMaxK = 32768;
+cudaError_t launch_fp8_act(const Fp8ActArgs& a, cudaStream_t s);
+
+// W [K, N] -> codes [N, K], scales [ceil(N/128), ceil(K/128)]
+cudaError_t launch_fp8_pack(int K, int N, const float* W, uint8_t* codes, float* scales, cudaStream_t s);
+
+struct Fp8GemmArgs {
+  const uint8_t* x_codes;     // [M, K]
+  const float* x_scales;      // [ceil(K/128), M]
+  const uint8_t* w_codes;     // [N, K]
+  const float* w_scales;      // [ceil(N/128), ceil(K/128)]
+  const uint16_t* bias;       // bf16 [N] or null
+  void* y;                    // [M, N] bf16 or fp32
+  int M, K, N;
+  int out_f32;
+  unsigned* err;
+  unsigned long long wait_ns;
+  int num_sms;
+};
+cudaError_t launch_fp8_linear(const Fp8GemmArgs& a, cudaStream_t s);
+
+constexpr int kRopeMaxPairs = 512;
+struct RopeArgs {
+  const long long* pos;       // [M, axes]
+  const double* freq;         // [pairs]
+  const int* axis;            // [pairs] or null
+  const uint16_t* x;          // bf16 [M, heads * head_dim], row stride ldx
+  uint16_t* y;                // same shape, row stride ldy (x itself: in place)
+  long long ldx, ldy;
+  int M, axes, pairs, heads, head_dim, half;
+  float factor;
+};
+cudaError_t launch_rope_apply(const RopeArgs& a, cudaStream_t s);
+cudaError_t launch_rope_tables(const RopeArgs& a, float* cos_t, float* sin_t, cudaStream_t s);
+
 cudaError_t launch_probe_convert(const float* in, long long n, uint8_t* e2m1, uint8_t* e4m3,
                                  uint16_t* bf16, cudaStream_t s);
 cudaError_t launch_probe_wait(unsigned* err, unsigned long long limit_ns, cudaStream_t s);

@@ -1,6 +1,7 @@
 /*
  * svdq.h — C ABI of the B200 (sm_100a) SVDQuant W4A4 and AWQ W4A16 linear
- * layers.
+ * layers, and of the 8-bit (E4M3) linear layer and rotary positions that stand
+ * beside them.
  *
  * The layer (blog "Introducing Nunchaku 4-bit inference in Diffusers",
  * section "Background: SVDQuant and Nunchaku"): SVDQuant migrates activation
@@ -246,6 +247,101 @@ svdq_status awq_pack_weight(int K, int N, const float* W, uint8_t* q, uint16_t* 
 svdq_status awq_w4a16_linear(int M, int K, int N, const uint16_t* x, const uint8_t* q,
                              const uint16_t* scales, const uint16_t* zeros, const uint16_t* bias,
                              uint16_t* y, void* stream);
+
+/* The 8-bit linear layer -----------------------------------------------------
+ * For layers that do not hold at 4 bits: E4M3 codes (round to nearest even,
+ * saturating at 448) with one fp32 scale per 128 columns of an activation row
+ * and per 128 x 128 block of a weight. K % 16 == 0; the last block of K (and,
+ * for weights, of N) may be short. G = ceil(K / 128).
+ *   activations: codes u8 [M, K], scales fp32 [G, M] (one block's row scales
+ *                contiguous for the GEMM epilogue)
+ *   weights:     codes u8 [N, K], scales fp32 [ceil(N/128), G]
+ * A block's scale is max(max|v| / 448, 2^-126), its codes e4m3(v / scale). A
+ * block that holds a NaN or an infinity stands for NaN throughout (its scale
+ * is NaN or infinite, its codes NaN or 0).
+ * Row strides (ldx, ...) are in elements, multiples of 8, at least the row's
+ * length; they may exceed it (a column range of a wider tensor). */
+
+/* svdq_fp8_quantize_act — the 8-bit form of bf16 activations.
+ * In:  x bf16 [M, K], row stride ldx. Out: codes, scales as above.
+ * Shapes: K >= 16, K % 16 == 0; M >= 0 (M = 0 is a no-op). Pointers 16-byte
+ * aligned. codes and scales overlap neither x nor each other
+ * (SVDQ_ERR_INVALID_ARG). */
+svdq_status svdq_fp8_quantize_act(int M, int K, const uint16_t* x, long long ldx, uint8_t* codes, float* scales,
+                                  void* stream);
+
+/* svdq_fp8_norm_quantize — the residual's addition, root-mean-square norm and
+ * the 8-bit form of the result, in one pass:
+ *   r = bf16(x + residual)          (r = x where residual is NULL)
+ *   v = r / sqrt(mean(r^2) + eps) * weight      (fp32, not rounded)
+ *   codes, scales of v as above
+ * In:  x bf16 [M, K] (row stride ldx); residual bf16 [M, K] (ldr) or NULL;
+ *      weight bf16 [K]; eps >= 0.
+ * Out: codes, scales; residual_out bf16 [M, K] (row stride ldo) = r, given
+ *      exactly when residual is. residual_out may be x or residual itself
+ *      (same address and stride); any other overlap of an output with an
+ *      input or another output gives SVDQ_ERR_INVALID_ARG.
+ * Shapes: as svdq_fp8_quantize_act, K <= 32768 (a row is held in registers).
+ * Pointers 16-byte aligned. */
+svdq_status svdq_fp8_norm_quantize(int M, int K, const uint16_t* x, long long ldx, const uint16_t* residual,
+                                   long long ldr, const uint16_t* weight, float eps, uint16_t* residual_out,
+                                   long long ldo, uint8_t* codes, float* scales, void* stream);
+
+/* svdq_fp8_pack_weight — offline pack of W fp32 [K, N] (y = x W).
+ * Out: codes u8 [N, K], scales fp32 [ceil(N/128), G].
+ * Shapes: K % 16 == 0, N % 8 == 0. Pointers 16-byte aligned. */
+svdq_status svdq_fp8_pack_weight(int K, int N, const float* W, uint8_t* codes, float* scales, void* stream);
+
+/* svdq_fp8_linear — the 8-bit GEMM:
+ *   y[m,n] = sum_g sx[g,m] sw[n/128,g] sum_{k in g} qx[m,k] qw[n,k] + bias[n]
+ * The products of a block are summed in fp32 by the tensor cores, the blocks
+ * in fp32; one rounding at the end. The order of the sums depends on the
+ * sizes alone, so a call repeated gives the same bits.
+ * In:  codes and scales of both operands; bias bf16 [N] or NULL.
+ * Out: y [M, N], bf16 (SVDQ_OUT_BF16) or fp32 (SVDQ_OUT_F32), overlapping no
+ *      input (SVDQ_ERR_INVALID_ARG); other output modes give
+ *      SVDQ_ERR_INVALID_ARG.
+ * Shapes: K % 16 == 0, N % 8 == 0, M >= 0 (M = 0 is a no-op). Codes and y
+ * 16-byte aligned, scales and bias 4-byte. */
+svdq_status svdq_fp8_linear(int M, int K, int N, const uint8_t* x_codes, const float* x_scales,
+                            const uint8_t* w_codes, const float* w_scales, const uint16_t* bias, void* y,
+                            svdq_out_dtype out, void* stream);
+
+/* Rotary positions -----------------------------------------------------------
+ * Pair i (0 <= i < pairs) of a head at row m turns by the angle
+ *   t[m,i] = pos[m, axis[i]] * freq[i]          (64 bits, reduced by whole
+ *                                                turns in 64 bits)
+ * with cos and sin multiplied by `factor`. pos int64 [M, axes] (negative
+ * positions turn back); freq fp64 [pairs], radians per position: every scaling
+ * for long contexts is a choice of freq and factor; axis int32 [pairs], values
+ * 0 .. axes - 1 (others read as 0), or NULL for all 0. */
+typedef enum {
+  SVDQ_ROPE_INTERLEAVED = 0, /* pair i = columns 2i, 2i + 1 of the head */
+  SVDQ_ROPE_HALF = 1         /* pair i = columns i, i + pairs */
+} svdq_rope_layout;
+
+/* svdq_rope_tables — cos and sin of t times factor, fp32 [M, pairs]: with
+ * pairs = 64 the tables that svdq_rope_pack and svdq_qkv_norm_rope take.
+ * Shapes: M >= 0 (M = 0 is a no-op), 1 <= axes <= 8, 1 <= pairs <= 512.
+ * pos, freq 8-byte aligned, axis, cos_t, sin_t 4-byte. The outputs overlap
+ * neither each other nor an input (SVDQ_ERR_INVALID_ARG). */
+svdq_status svdq_rope_tables(int M, int axes, int pairs, const long long* pos, const double* freq, const int* axis,
+                             float factor, float* cos_t, float* sin_t, void* stream);
+
+/* svdq_rope_apply — rotates the heads of x bf16 [M, heads * head_dim] (row
+ * stride ldx): columns 0 .. 2 pairs - 1 of each head as
+ *   a' = a cos t - b sin t, b' = a sin t + b cos t   (fp32, rounded once)
+ * the columns past them unchanged. The Q and K sections of a grouped Q/K/V
+ * row are adjacent, so one call with heads = query + key heads rotates both.
+ * Out: y bf16 [M, heads * head_dim] (row stride ldy); y may be x itself (same
+ *      address and stride: in place, only the rotated columns are touched);
+ *      any other overlap gives SVDQ_ERR_INVALID_ARG.
+ * Shapes: M >= 0 (M = 0 is a no-op), 1 <= pairs <= 512, 2 pairs <= head_dim,
+ * head_dim % 8 == 0, heads * head_dim <= 2^20. x, y 16-byte aligned; the
+ * others as svdq_rope_tables. */
+svdq_status svdq_rope_apply(int M, int heads, int head_dim, int pairs, svdq_rope_layout layout, int axes,
+                            const long long* pos, const double* freq, const int* axis, float factor,
+                            const uint16_t* x, long long ldx, uint16_t* y, long long ldy, void* stream);
 
 /* Reads and clears the device error word of the current device: bit 0 = a
  * bounded wait ran out, bit 1 = a kernel saw an inconsistent launch. The
