@@ -1,61 +1,350 @@
-// The 8-bit GEMM (svdq_fp8_linear):
+// The 8-bit GEMM (svdq_fp8_linear) for many rows:
 //   y[m,n] = sum_g sx[g,m] sw[n/128,g] sum_{k in g} qx[m,k] qw[n,k] + bias[n]
-// with E4M3 codes and fp32 scales per 128 columns of K. A 64 x 64 output tile
-// per CTA, the operands converted to fp32 in shared memory.
-#include "device.cuh"
+//
+// A block's product is one accumulator of the tensor cores; the scales are
+// fp32 and differ from block to block of 128 along K, so a block's sums leave
+// tensor memory before the next block may use their place, and are added,
+// scaled, to sums in registers. That drain (one fused multiply-add for every
+// 128 products) is the second bound beside the MMA rate: 32,768 sums per SM
+// and K block of 512 MMA cycles.
+//
+// Persistent, warp-specialised CTA pairs (cluster of 2, cta_group::2), each
+// with a 256 x 256 tile of y:
+//   warp 0       TMA producer (both CTAs): per K block this CTA's 128 rows of A
+//                and 128 rows of B, 128-byte rows, 128B-swizzled
+//   warp 1       MMA issuer (leader CTA): per K block two products of N = 128
+//                (column halves), each into one of its half's two accumulators
+//   warp 2       tensor-memory allocation
+//   warps 4..11  drain (both CTAs), two warps per lane quadrant, one for each
+//                column half: a thread is a row, its 128 sums stay in
+//                registers over the whole K loop. A half is one 128-wide
+//                weight block, so a K block has one combined scale per thread.
+//                At the end bias, rounding, TMA store through 4 KB of staging.
+// Four accumulators of 128 columns (rather than two of 256): while one is
+// drained and handed back the other three take 768 cycles of MMAs.
+#include "fp8.cuh"
 #include "kernels.h"
 
 namespace svdq {
 namespace {
 
-__global__ void __launch_bounds__(256) gemm_fp8_kernel(Fp8GemmArgs a) {
-  __shared__ float sx[32][65], sw[32][65];
-  const int n0 = blockIdx.x * 64, m0 = blockIdx.y * 64;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int G = (a.K + 127) / 128;
-  float acc[4][4] = {}, part[4][4] = {};
-  for (int k0 = 0; k0 < a.K; k0 += 32) {
-    for (int i = threadIdx.x; i < 64 * 32; i += 256) {
-      const int r = i >> 5, k = i & 31;
-      const bool in = k0 + k < a.K;
-      sx[k][r] = in && m0 + r < a.M ? e4m3_to_f32(a.x_codes[(size_t)(m0 + r) * a.K + k0 + k]) : 0.f;
-      sw[k][r] = in && n0 + r < a.N ? e4m3_to_f32(a.w_codes[(size_t)(n0 + r) * a.K + k0 + k]) : 0.f;
+constexpr int BM = 128, BN = 256, BK = 128;   // rows per CTA, columns per pair, bytes of K per stage
+constexpr int kStages = 6;
+constexpr int kABytes = BM * BK;
+constexpr int kBBytes = (BN / 2) * BK;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kDrainWarps = 8;
+constexpr int kThreads = 128 + 32 * kDrainWarps;
+constexpr int kSlotBytes = 32 * 128;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kIdesc = f8_idesc(2 * BM, 128);
+constexpr int kGroupM = 8;                     // row tiles that share their column tiles in time
+// shares of the 384 x 168 registers of a launch: 256 x 216 + 128 x 72
+constexpr int kDrainRegs = 216, kOtherRegs = 72;
+static_assert(256 * kDrainRegs + 128 * kOtherRegs <= kThreads * 168, "register shares");
+
+struct Smem {
+  uint8_t stage[kStages][kStageBytes];
+  uint8_t out[kDrainWarps][kSlotBytes];
+  uint64_t full[kStages], empty[kStages];
+  uint64_t acc_full[4], acc_free[4], mma_done;
+  uint32_t tmem_base;
+};
+
+struct Params {
+  const float* x_scales;
+  const float* w_scales;
+  const uint16_t* bias;
+  int M, N, K, G;
+  int tiles_m, tiles_n;    // 256-row and 256-column tiles
+  int out_f32;
+  unsigned* err;
+  unsigned long long wait_ns;
+};
+
+// Tiles in groups of kGroupM tile rows, down the rows first: the tiles in
+// work at one time span about as many rows as columns, so that both operands
+// are read from L2 rather than HBM.
+__device__ __forceinline__ void tile_at(int t, const Params& p, int& tm, int& tn) {
+  const int per = kGroupM * p.tiles_n;
+  const int g = t / per, r = t % per;
+  const int rows = min(kGroupM, p.tiles_m - g * kGroupM);
+  tm = g * kGroupM + r % rows;
+  tn = r / rows;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                const __grid_constant__ CUtensorMap tm_y, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(smem_align<1024>(smem_raw));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int num_tiles = p.tiles_m * p.tiles_n;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
     }
-    __syncthreads();
-    for (int k = 0; k < 32; ++k)
-      for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) part[i][j] = fmaf(sx[k][ty + 16 * i], sw[k][tx + 16 * j], part[i][j]);
-    __syncthreads();
-    if (k0 % 128 == 96 || k0 + 32 >= a.K) {
-      const int g = k0 / 128;
-      for (int i = 0; i < 4; ++i) {
-        const int m = m0 + ty + 16 * i;
-        const float s = m < a.M ? a.x_scales[(size_t)g * a.M + m] : 0.f;
-        for (int j = 0; j < 4; ++j) {
-          const int n = n0 + tx + 16 * j;
-          if (n < a.N) acc[i][j] = fmaf(s * a.w_scales[(size_t)(n / 128) * G + g], part[i][j], acc[i][j]);
-          part[i][j] = 0.f;
+    for (int b = 0; b < 4; ++b) {
+      mbar_init(&sm.acc_full[b], 1);
+      mbar_init(&sm.acc_free[b], 8);   // four warps of each CTA
+    }
+    mbar_init(&sm.mma_done, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+    tma_prefetch_desc(&tm_y);
+  }
+  if (warp == 2) {
+    __syncwarp();
+    tmem_alloc_pair(&sm.tmem_base, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  // every input may be the previous kernel's output, y may still be read by it
+  if (threadIdx.x == 0) launch_dependents();
+  grid_dependency_wait();
+
+  if (warp < 4) {
+    regs_dec<kOtherRegs>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      if (lane == 0) {
+        uint32_t it = 0;
+        bool ok = true;
+        for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
+          int tm, tn;
+          tile_at(tile, p, tm, tn);
+          const int row0 = tm * 256 + (int)rank * BM;
+          const int col0 = tn * BN + (int)rank * 64;   // columns col0.. and col0 + 128.., 64 each
+          for (int kb = 0; kb < p.G; ++kb, ++it) {
+            const int s = it % kStages;
+            if (!mbar_wait(&sm.empty[s], ((it / kStages) & 1) ^ 1, p.wait_ns, p.err)) { ok = false; break; }
+            uint8_t* st = sm.stage[s];
+            const uint32_t fb = mapa_shared(smem_u32(&sm.full[s]), 0);
+            if (leader) mbar_expect_tx(&sm.full[s], 2 * kStageBytes);
+            tma_load_2d_pair(st, &tm_a, fb, kb * BK, row0);
+            tma_load_2d_pair(st + kABytes, &tm_b, fb, kb * BK, col0);
+            tma_load_2d_pair(st + kABytes + 64 * BK, &tm_b, fb, kb * BK, col0 + 128);
+          }
+        }
+        if (!ok && leader) {
+          // let the copies already issued by both CTAs land before the pair exits
+          for (uint32_t d = 1; d <= (uint32_t)kStages && d <= it; ++d) {
+            const uint32_t j = it - d;
+            (void)mbar_wait(&sm.full[j % kStages], (j / kStages) & 1, p.wait_ns, nullptr);
+          }
+        }
+      }
+    } else if (warp == 1 && leader) {
+      // ---------------------------------------------------------- MMA issuer
+      uint32_t it = 0;
+      bool ok = true;
+      for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
+        for (int kb = 0; kb < p.G; ++kb, ++it) {
+          const int s = it % kStages;
+          if (!warp_wait(&sm.full[s], (it / kStages) & 1, p.wait_ns, p.err)) { ok = false; break; }
+          const uint32_t st = smem_u32(sm.stage[s]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int b = 2 * (it & 1) + h;
+            if (!__all_sync(0xffffffffu, mbar_wait_cluster(&sm.acc_free[b], ((it >> 1) & 1) ^ 1, p.wait_ns, p.err))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            uint64_t da[4], db[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              da[j] = make_sdesc(st + 32 * j, 16, 1024, kLayoutSw128);
+              db[j] = make_sdesc(st + kABytes + h * 64 * BK + 32 * j, 16, 1024, kLayoutSw128);
+            }
+            if (elect_one()) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) mma_f8_pair(tmem + 128 * b, da[j], db[j], kIdesc, j > 0 ? 1u : 0u);
+              tc_commit_pair(&sm.acc_full[b], 0x3);
+              if (h == 1) tc_commit_pair(&sm.empty[s], 0x3);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+        }
+      }
+      // every MMA issued has completed before tensor memory is freed
+      if (elect_one()) tc_commit_pair(&sm.mma_done, 0x1);
+      __syncwarp();
+      (void)warp_wait(&sm.mma_done, 0, p.wait_ns, p.err);
+    }
+  } else {
+    // ------------------------------------------------------------ drain
+    regs_inc<kDrainRegs>();
+    const int q = warp & 3, e = warp - 4, h = e >> 2;
+    uint8_t* buf = sm.out[e];
+    uint32_t it = 0;
+    bool ok = true;
+    for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
+      int tm, tn;
+      tile_at(tile, p, tm, tn);
+      const int row0 = tm * 256 + (int)rank * BM + 32 * q;
+      const int n0 = tn * BN + 128 * h;
+      // rows and columns past the end are not stored: any scale will do
+      const float* sxp = p.x_scales + min(row0 + lane, p.M - 1);
+      const float* swp = p.w_scales + (size_t)min(n0 / 128, (p.N - 1) / 128) * p.G;
+      float2 acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
+      float sx = __ldg(sxp), sw = __ldg(swp);
+#pragma unroll 1
+      for (int kb = 0; kb < p.G; ++kb, ++it) {
+        const int b = 2 * (it & 1) + h;
+        const float s = sx * sw;
+        if (kb + 1 < p.G) {
+          sx = __ldg(sxp + (size_t)(kb + 1) * p.M);
+          sw = __ldg(swp + kb + 1);
+        }
+        if (!warp_wait(&sm.acc_full[b], (it >> 1) & 1, p.wait_ns, p.err)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t tb = tmem + 128 * b + ((uint32_t)(32 * q) << 16);
+        const float2 s2 = make_float2(s, s);
+        uint32_t v[2][32];
+        tmem_ld32(tb, v[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld_wait();
+          tmem_regs_ready(v[c & 1]);
+          if (c < 3) {
+            tmem_ld32(tb + 32 * (c + 1), v[(c + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sm.acc_free[b]), 0));
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            acc[16 * c + i] = __ffma2_rn(
+                make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), s2, acc[16 * c + i]);
+        }
+      }
+      if (!ok) break;
+      // ---- output: 128 columns in pieces of 128 bytes a row
+      if (p.out_f32) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int n = n0 + 32 * c;
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            float2 lo = acc[16 * c + 2 * u], hi = acc[16 * c + 2 * u + 1];
+            if (p.bias && n + 4 * u < p.N) {
+              const uint32_t b0 = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n + 4 * u));
+              const uint32_t b1 = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n + 4 * u + 2));
+              lo.x += bf16_bits_to_f32(b0 & 0xFFFFu);
+              lo.y += bf16_bits_to_f32(b0 >> 16);
+              hi.x += bf16_bits_to_f32(b1 & 0xFFFFu);
+              hi.y += bf16_bits_to_f32(b1 >> 16);
+            }
+            *reinterpret_cast<float4*>(buf + lane * 128 + ((u ^ (lane & 7)) * 16)) = make_float4(lo.x, lo.y, hi.x, hi.y);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (row0 < p.M && n < p.N) tma_store_2d(&tm_y, buf, n, row0);
+            bulk_commit();
+          }
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int n = n0 + 64 * c;
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            uint32_t w4[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float2 a = acc[32 * c + 4 * u + k];
+              if (p.bias && n + 8 * u < p.N) {
+                const uint32_t bw = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n + 8 * u + 2 * k));
+                a.x += bf16_bits_to_f32(bw & 0xFFFFu);
+                a.y += bf16_bits_to_f32(bw >> 16);
+              }
+              w4[k] = f32_to_bf16_bits(a.x) | (f32_to_bf16_bits(a.y) << 16);
+            }
+            *reinterpret_cast<uint4*>(buf + lane * 128 + ((u ^ (lane & 7)) * 16)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (row0 < p.M && n < p.N) tma_store_2d(&tm_y, buf, n, row0);
+            bulk_commit();
+          }
         }
       }
     }
+    if (lane == 0) bulk_wait<0>();
+    __syncwarp();
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m >= a.M || n >= a.N) continue;
-      const float y = acc[i][j] + (a.bias ? bf16_bits_to_f32(a.bias[n]) : 0.f);
-      if (a.out_f32)
-        static_cast<float*>(a.y)[(size_t)m * a.N + n] = y;
-      else
-        static_cast<uint16_t*>(a.y)[(size_t)m * a.N + n] = (uint16_t)f32_to_bf16_bits(y);
-    }
+
+  __syncwarp();  // the cluster barrier is .aligned: every warp reconverges first
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+  __syncwarp();
+  cluster_sync();
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_linear(const Fp8GemmArgs& a, cudaStream_t s) {
-  const dim3 grid((a.N + 63) / 64, (a.M + 63) / 64);
-  gemm_fp8_kernel<<<grid, 256, 0, s>>>(a);
+  CUtensorMap tm_a, tm_b, tm_y;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  bool ok = make_tmap_2d(&tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.x_codes, a.K, a.M, a.K, BK, BM, sw) &&
+            make_tmap_2d(&tm_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w_codes, a.K, a.N, a.K, BK, 64, sw);
+  if (a.out_f32)
+    ok = ok && make_tmap_2d(&tm_y, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.y, a.N, a.M, (uint64_t)a.N * 4, 32, 32, sw);
+  else
+    ok = ok && make_tmap_2d(&tm_y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.y, a.N, a.M, (uint64_t)a.N * 2, 64, 32, sw);
+  if (!ok) return cudaErrorInvalidValue;
+  Params p;
+  p.x_scales = a.x_scales;
+  p.w_scales = a.w_scales;
+  p.bias = a.bias;
+  p.M = a.M; p.N = a.N; p.K = a.K;
+  p.G = (a.K + 127) / 128;
+  p.tiles_m = (a.M + 255) / 256;
+  p.tiles_n = (a.N + BN - 1) / BN;
+  p.out_f32 = a.out_f32;
+  p.err = a.err;
+  p.wait_ns = a.wait_ns;
+  const size_t smem = sizeof(Smem) + 1024;
+  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(gemm_fp8_kernel), (int)smem);
+  if (e != cudaSuccess) return e;
+  const int tiles = p.tiles_m * p.tiles_n, pairs = a.num_sms / 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (tiles < pairs ? tiles : pairs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, gemm_fp8_kernel, tm_a, tm_b, tm_y, p);
+  if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
