@@ -41,6 +41,37 @@ constexpr uint32_t f8_idesc(int m, int n) {
   return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
+// One arrival on an mbarrier of the cluster, and the wait for it, where the
+// barrier hands over tensor memory alone: the loads from it have returned
+// (tcgen05.wait::ld) and the tcgen05 fences order what follows, so neither
+// side orders other memory. A release at cluster scope in the drain's inner
+// loop waited for every earlier access of the warp (it was the largest stall).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_relaxed(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_relaxed(uint64_t* bar, uint32_t parity, uint64_t limit_ns, unsigned* err) {
+  if (mbar_try_wait_relaxed(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (mbar_try_wait_relaxed(bar, parity)) return true;
+    if (globaltimer_ns() - t0 > limit_ns) {
+      raise_error(err, kErrTimeout);
+      return false;
+    }
+  }
+}
+
 // Register shares of a warpgroup (all four warps execute it).
 template <int N>
 __device__ __forceinline__ void regs_inc() {

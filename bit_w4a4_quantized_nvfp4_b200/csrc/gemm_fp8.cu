@@ -156,7 +156,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int b = 2 * (it & 1) + h;
-            if (!__all_sync(0xffffffffu, mbar_wait_cluster(&sm.acc_free[b], ((it >> 1) & 1) ^ 1, p.wait_ns, p.err))) {
+            if (!__all_sync(0xffffffffu, mbar_wait_relaxed(&sm.acc_free[b], ((it >> 1) & 1) ^ 1, p.wait_ns, p.err))) {
               ok = false;
               break;
             }
@@ -225,7 +225,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           } else {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sm.acc_free[b]), 0));
+            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&sm.acc_free[b]), 0));
           }
 #pragma unroll
           for (int i = 0; i < 16; ++i)
