@@ -29,15 +29,15 @@ namespace svdq {
 namespace {
 
 constexpr int BM = 128, BN = 256, BK = 128;   // rows per CTA, columns per pair, bytes of K per stage
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kABytes = BM * BK;
 constexpr int kBBytes = (BN / 2) * BK;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kDrainWarps = 8;
 constexpr int kThreads = 128 + 32 * kDrainWarps;
-constexpr int kSlotBytes = 32 * 128;
+constexpr int kSlots = 2, kSlotBytes = 32 * 128;   // output staging per drain warp
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kIdesc = f8_idesc(2 * BM, 128);
+constexpr uint32_t kIdesc = f8_idesc(2 * BM, BN);
 constexpr int kGroupM = 8;                     // row tiles that share their column tiles in time
 // shares of the 384 x 168 registers of a launch: 256 x 216 + 128 x 72
 constexpr int kDrainRegs = 216, kOtherRegs = 72;
@@ -45,9 +45,9 @@ static_assert(256 * kDrainRegs + 128 * kOtherRegs <= kThreads * 168, "register s
 
 struct Smem {
   uint8_t stage[kStages][kStageBytes];
-  uint8_t out[kDrainWarps][kSlotBytes];
+  uint8_t out[kDrainWarps][kSlots][kSlotBytes];
   uint64_t full[kStages], empty[kStages];
-  uint64_t acc_full[4], acc_free[4], mma_done;
+  uint64_t acc_full[2], acc_free[2], mma_done;
   uint32_t tmem_base;
 };
 
@@ -89,9 +89,9 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       mbar_init(&sm.full[s], 1);
       mbar_init(&sm.empty[s], 1);
     }
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.acc_full[b], 1);
-      mbar_init(&sm.acc_free[b], 8);   // four warps of each CTA
+      mbar_init(&sm.acc_free[b], 2 * kDrainWarps);
     }
     mbar_init(&sm.mma_done, 1);
     fence_mbar_init();
@@ -124,7 +124,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           int tm, tn;
           tile_at(tile, p, tm, tn);
           const int row0 = tm * 256 + (int)rank * BM;
-          const int col0 = tn * BN + (int)rank * 64;   // columns col0.. and col0 + 128.., 64 each
+          const int col0 = tn * BN + (int)rank * (BN / 2);
           for (int kb = 0; kb < p.G; ++kb, ++it) {
             const int s = it % kStages;
             if (!mbar_wait(&sm.empty[s], ((it / kStages) & 1) ^ 1, p.wait_ns, p.err)) { ok = false; break; }
@@ -133,7 +133,6 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
             if (leader) mbar_expect_tx(&sm.full[s], 2 * kStageBytes);
             tma_load_2d_pair(st, &tm_a, fb, kb * BK, row0);
             tma_load_2d_pair(st + kABytes, &tm_b, fb, kb * BK, col0);
-            tma_load_2d_pair(st + kABytes + 64 * BK, &tm_b, fb, kb * BK, col0 + 128);
           }
         }
         if (!ok && leader) {
@@ -153,29 +152,25 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           const int s = it % kStages;
           if (!warp_wait(&sm.full[s], (it / kStages) & 1, p.wait_ns, p.err)) { ok = false; break; }
           const uint32_t st = smem_u32(sm.stage[s]);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int b = 2 * (it & 1) + h;
-            if (!__all_sync(0xffffffffu, mbar_wait_relaxed(&sm.acc_free[b], ((it >> 1) & 1) ^ 1, p.wait_ns, p.err))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            uint64_t da[4], db[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              da[j] = make_sdesc(st + 32 * j, 16, 1024, kLayoutSw128);
-              db[j] = make_sdesc(st + kABytes + h * 64 * BK + 32 * j, 16, 1024, kLayoutSw128);
-            }
-            if (elect_one()) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) mma_f8_pair(tmem + 128 * b, da[j], db[j], kIdesc, j > 0 ? 1u : 0u);
-              tc_commit_pair(&sm.acc_full[b], 0x3);
-              if (h == 1) tc_commit_pair(&sm.empty[s], 0x3);
-            }
-            __syncwarp();
+          const int b = it & 1;
+          if (!__all_sync(0xffffffffu, mbar_wait_relaxed(&sm.acc_free[b], ((it >> 1) & 1) ^ 1, p.wait_ns, p.err))) {
+            ok = false;
+            break;
           }
-          if (!ok) break;
+          tc_fence_after();
+          uint64_t da[4], db[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            da[j] = make_sdesc(st + 32 * j, 16, 1024, kLayoutSw128);
+            db[j] = make_sdesc(st + kABytes + 32 * j, 16, 1024, kLayoutSw128);
+          }
+          if (elect_one()) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mma_f8_pair(tmem + BN * b, da[j], db[j], kIdesc, j > 0 ? 1u : 0u);
+            tc_commit_pair(&sm.acc_full[b], 0x3);
+            tc_commit_pair(&sm.empty[s], 0x3);
+          }
+          __syncwarp();
         }
       }
       // every MMA issued has completed before tensor memory is freed
@@ -187,7 +182,6 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     // ------------------------------------------------------------ drain
     regs_inc<kDrainRegs>();
     const int q = warp & 3, e = warp - 4, h = e >> 2;
-    uint8_t* buf = sm.out[e];
     uint32_t it = 0;
     bool ok = true;
     for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
@@ -201,36 +195,48 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       float2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
-      float sx = __ldg(sxp), sw = __ldg(swp);
+      // a K block's scale is loaded two blocks ahead of its use
+      float sx[2], sw[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int kb = min(j, p.G - 1);
+        sx[j] = __ldg(sxp + (size_t)kb * p.M);
+        sw[j] = __ldg(swp + kb);
+      }
 #pragma unroll 1
-      for (int kb = 0; kb < p.G; ++kb, ++it) {
-        const int b = 2 * (it & 1) + h;
-        const float s = sx * sw;
-        if (kb + 1 < p.G) {
-          sx = __ldg(sxp + (size_t)(kb + 1) * p.M);
-          sw = __ldg(swp + kb + 1);
-        }
-        if (!warp_wait(&sm.acc_full[b], (it >> 1) & 1, p.wait_ns, p.err)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t tb = tmem + 128 * b + ((uint32_t)(32 * q) << 16);
-        const float2 s2 = make_float2(s, s);
-        uint32_t v[2][32];
-        tmem_ld32(tb, v[0]);
+      for (int kb0 = 0; kb0 < p.G && ok; kb0 += 2) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld_wait();
-          tmem_regs_ready(v[c & 1]);
-          if (c < 3) {
-            tmem_ld32(tb + 32 * (c + 1), v[(c + 1) & 1]);
-          } else {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&sm.acc_free[b]), 0));
+        for (int j = 0; j < 2; ++j) {
+          if (kb0 + j >= p.G) break;
+          const int b = it & 1;
+          const float s = sx[j] * sw[j];
+          if (kb0 + j + 2 < p.G) {
+            sx[j] = __ldg(sxp + (size_t)(kb0 + j + 2) * p.M);
+            sw[j] = __ldg(swp + kb0 + j + 2);
           }
+          if (!warp_wait(&sm.acc_full[b], (it >> 1) & 1, p.wait_ns, p.err)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t tb = tmem + BN * b + 128 * h + ((uint32_t)(32 * q) << 16);
+          const float2 s2 = make_float2(s, s);
+          uint32_t v[2][16];
+          tmem_ld16(tb, v[0]);
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            acc[16 * c + i] = __ffma2_rn(
-                make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), s2, acc[16 * c + i]);
+          for (int c = 0; c < 8; ++c) {
+            tmem_ld_wait();
+            tmem_regs_ready(v[c & 1]);
+            if (c < 7) {
+              tmem_ld16(tb + 16 * (c + 1), v[(c + 1) & 1]);
+            } else {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&sm.acc_free[b]), 0));
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              acc[8 * c + i] = __ffma2_rn(
+                  make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), s2, acc[8 * c + i]);
+          }
+          ++it;
         }
       }
       if (!ok) break;
@@ -239,7 +245,8 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int n = n0 + 32 * c;
-          if (lane == 0) bulk_wait_read<0>();
+          uint8_t* buf = sm.out[e][c % kSlots];
+          if (lane == 0) bulk_wait_read<kSlots - 1>();
           __syncwarp();
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
@@ -265,7 +272,8 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int n = n0 + 64 * c;
-          if (lane == 0) bulk_wait_read<0>();
+          uint8_t* buf = sm.out[e][c % kSlots];
+          if (lane == 0) bulk_wait_read<kSlots - 1>();
           __syncwarp();
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
@@ -312,7 +320,7 @@ cudaError_t launch_fp8_linear(const Fp8GemmArgs& a, cudaStream_t s) {
   CUtensorMap tm_a, tm_b, tm_y;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
   bool ok = make_tmap_2d(&tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.x_codes, a.K, a.M, a.K, BK, BM, sw) &&
-            make_tmap_2d(&tm_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w_codes, a.K, a.N, a.K, BK, 64, sw);
+            make_tmap_2d(&tm_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w_codes, a.K, a.N, a.K, BK, BN / 2, sw);
   if (a.out_f32)
     ok = ok && make_tmap_2d(&tm_y, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.y, a.N, a.M, (uint64_t)a.N * 4, 32, 32, sw);
   else
