@@ -46,8 +46,12 @@ constexpr uint32_t f8_idesc(int m, int n) {
 // (tcgen05.wait::ld) and the tcgen05 fences order what follows, so neither
 // side orders other memory. A release at cluster scope in the drain's inner
 // loop waited for every earlier access of the warp (it was the largest stall).
-__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+__device__ __forceinline__ void mbar_arrive_if(bool on, uint32_t cluster_addr) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_addr), "r"((uint32_t)on)
+      : "memory");
 }
 __device__ __forceinline__ bool mbar_try_wait_relaxed(uint64_t* bar, uint32_t parity) {
   uint32_t ok;

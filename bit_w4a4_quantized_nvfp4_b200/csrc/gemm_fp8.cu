@@ -37,7 +37,8 @@ constexpr int kDrainWarps = 8;
 constexpr int kThreads = 128 + 32 * kDrainWarps;
 constexpr int kSlots = 2, kSlotBytes = 32 * 128;   // output staging per drain warp
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kIdesc = f8_idesc(2 * BM, BN);
+constexpr int UN = 128;                        // columns of a unit: one accumulator
+constexpr uint32_t kIdesc = f8_idesc(2 * BM, UN);
 constexpr int kGroupM = 8;                     // row tiles that share their column tiles in time
 // shares of the 384 x 168 registers of a launch: 256 x 216 + 128 x 72
 constexpr int kDrainRegs = 216, kOtherRegs = 72;
@@ -47,7 +48,7 @@ struct Smem {
   uint8_t stage[kStages][kStageBytes];
   uint8_t out[kDrainWarps][kSlots][kSlotBytes];
   uint64_t full[kStages], empty[kStages];
-  uint64_t acc_full[2], acc_free[2], mma_done;
+  uint64_t acc_full[4], acc_free[4], mma_done;
   uint32_t tmem_base;
 };
 
@@ -87,13 +88,13 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.empty[s], 1);
+      mbar_init(&sm.empty[s], 2);   // both issuers
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < 4; ++b) {
       mbar_init(&sm.acc_full[b], 1);
       mbar_init(&sm.acc_free[b], 2 * kDrainWarps);
     }
-    mbar_init(&sm.mma_done, 1);
+    mbar_init(&sm.mma_done, 2);
     fence_mbar_init();
     tma_prefetch_desc(&tm_a);
     tma_prefetch_desc(&tm_b);
@@ -124,7 +125,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           int tm, tn;
           tile_at(tile, p, tm, tn);
           const int row0 = tm * 256 + (int)rank * BM;
-          const int col0 = tn * BN + (int)rank * (BN / 2);
+          const int col0 = tn * BN + (int)rank * (UN / 2);   // this CTA's half of each unit's columns
           for (int kb = 0; kb < p.G; ++kb, ++it) {
             const int s = it % kStages;
             if (!mbar_wait(&sm.empty[s], ((it / kStages) & 1) ^ 1, p.wait_ns, p.err)) { ok = false; break; }
@@ -133,6 +134,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
             if (leader) mbar_expect_tx(&sm.full[s], 2 * kStageBytes);
             tma_load_2d_pair(st, &tm_a, fb, kb * BK, row0);
             tma_load_2d_pair(st + kABytes, &tm_b, fb, kb * BK, col0);
+            tma_load_2d_pair(st + kABytes + kBBytes / 2, &tm_b, fb, kb * BK, col0 + UN);
           }
         }
         if (!ok && leader) {
@@ -143,34 +145,40 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           }
         }
       }
-    } else if (warp == 1 && leader) {
-      // ---------------------------------------------------------- MMA issuer
-      uint32_t it = 0;
+    } else if ((warp == 1 || warp == 3) && leader) {
+      // ---------------------------------------------------------- MMA issuers
+      const int h = warp >> 1;
+      // descriptors of stage 0; a stage further is kStageBytes further, a K
+      // step of 32 bytes 2 (addresses are in units of 16 bytes)
+      const uint64_t a0 = make_sdesc(smem_u32(sm.stage[0]), 16, 1024, kLayoutSw128);
+      const uint64_t b0 = make_sdesc(smem_u32(sm.stage[0]) + kABytes + h * (kBBytes / 2), 16, 1024, kLayoutSw128);
+      uint32_t it = 0, s = 0, sph = 0;   // K block, its stage and that stage's phase
       bool ok = true;
       for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
         for (int kb = 0; kb < p.G; ++kb, ++it) {
-          const int s = it % kStages;
-          if (!warp_wait(&sm.full[s], (it / kStages) & 1, p.wait_ns, p.err)) { ok = false; break; }
-          const uint32_t st = smem_u32(sm.stage[s]);
-          const int b = it & 1;
-          if (!__all_sync(0xffffffffu, mbar_wait_relaxed(&sm.acc_free[b], ((it >> 1) & 1) ^ 1, p.wait_ns, p.err))) {
+          const uint32_t b = 2 * (it & 1) + h, aph = ((it >> 1) & 1) ^ 1;
+          // both barriers tested at once: a test takes some 140 cycles
+          const bool rf = mbar_try_wait_relaxed(&sm.acc_free[b], aph);
+          const bool rs = mbar_try_wait(&sm.full[s], sph);
+          if (!__all_sync(0xffffffffu, rs && rf) &&
+              !(warp_wait(&sm.full[s], sph, p.wait_ns, p.err) &&
+                __all_sync(0xffffffffu, mbar_wait_relaxed(&sm.acc_free[b], aph, p.wait_ns, p.err)))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          uint64_t da[4], db[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            da[j] = make_sdesc(st + 32 * j, 16, 1024, kLayoutSw128);
-            db[j] = make_sdesc(st + kABytes + 32 * j, 16, 1024, kLayoutSw128);
-          }
+          const uint64_t da = a0 + (uint64_t)(s * (kStageBytes >> 4)), db = b0 + (uint64_t)(s * (kStageBytes >> 4));
           if (elect_one()) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mma_f8_pair(tmem + BN * b, da[j], db[j], kIdesc, j > 0 ? 1u : 0u);
+            for (int j = 0; j < 4; ++j) mma_f8_pair(tmem + UN * b, da + 2 * j, db + 2 * j, kIdesc, j > 0 ? 1u : 0u);
             tc_commit_pair(&sm.acc_full[b], 0x3);
             tc_commit_pair(&sm.empty[s], 0x3);
           }
           __syncwarp();
+          if (++s == kStages) {
+            s = 0;
+            sph ^= 1;
+          }
         }
       }
       // every MMA issued has completed before tensor memory is freed
@@ -181,62 +189,88 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
   } else {
     // ------------------------------------------------------------ drain
     regs_inc<kDrainRegs>();
-    const int q = warp & 3, e = warp - 4, h = e >> 2;
+    const int q = warp & 3, e = warp - 4, w = e >> 2;
+    const uint32_t tq = tmem + 64 * w + ((uint32_t)(32 * q) << 16);
+    const uint32_t free0 = mapa_shared(smem_u32(&sm.acc_free[0]), 0);
     uint32_t it = 0;
     bool ok = true;
     for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
       int tm, tn;
       tile_at(tile, p, tm, tn);
       const int row0 = tm * 256 + (int)rank * BM + 32 * q;
-      const int n0 = tn * BN + 128 * h;
+      const int n0 = tn * BN + 64 * w;
       // rows and columns past the end are not stored: any scale will do
       const float* sxp = p.x_scales + min(row0 + lane, p.M - 1);
-      const float* swp = p.w_scales + (size_t)min(n0 / 128, (p.N - 1) / 128) * p.G;
-      float2 acc[64];
+      const float* swp = p.w_scales + (size_t)(2 * tn) * p.G;
+      const size_t sw1 = 2 * tn + 1 <= (p.N - 1) / 128 ? p.G : 0;
+      float2 acc[64];   // columns n0 .. n0 + 63, then n0 + 128 .. n0 + 191
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
-      // a K block's scale is loaded two blocks ahead of its use
-      float sx[2], sw[2];
+      // a K block's scales are loaded two blocks ahead of their use: beside
+      // the tiles' loads a read of L2 can take longer than one block
+      float sx[2], swa[2], swb[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int kb = min(j, p.G - 1);
         sx[j] = __ldg(sxp + (size_t)kb * p.M);
-        sw[j] = __ldg(swp + kb);
+        swa[j] = __ldg(swp + kb);
+        swb[j] = __ldg(swp + sw1 + kb);
       }
+      // The units' sums are read as one stream of 16-column steps: the next
+      // step's load is in flight during this step's multiply-adds, across
+      // units too. The next unit's barrier is tested (not waited for) ahead,
+      // since a test takes some 150 cycles beside the MMAs' shared-memory reads.
+      if (!warp_wait(&sm.acc_full[2 * (it & 1)], (it >> 1) & 1, p.wait_ns, p.err)) break;
+      tc_fence_after();
+      uint32_t v[2][16];
+      tmem_ld16(tq + 2 * UN * (it & 1), v[0]);
 #pragma unroll 1
       for (int kb0 = 0; kb0 < p.G && ok; kb0 += 2) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (kb0 + j >= p.G) break;
-          const int b = it & 1;
-          const float s = sx[j] * sw[j];
-          if (kb0 + j + 2 < p.G) {
-            sx[j] = __ldg(sxp + (size_t)(kb0 + j + 2) * p.M);
-            sw[j] = __ldg(swp + kb0 + j + 2);
-          }
-          if (!warp_wait(&sm.acc_full[b], (it >> 1) & 1, p.wait_ns, p.err)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t tb = tmem + BN * b + 128 * h + ((uint32_t)(32 * q) << 16);
+        for (int jh = 0; jh < 4; ++jh) {
+          const int j = jh >> 1, h = jh & 1, kb = kb0 + j;
+          if (kb >= p.G) break;
+          const uint32_t b = 2 * (it & 1) + h;
+          const uint32_t tb = tq + UN * b;
+          // the unit after this one: the other half, or the next K block's first
+          const uint32_t nb = h == 0 ? b + 1 : 2 * (~it & 1);
+          const uint32_t npar = ((h == 0 ? it : it + 1) >> 1) & 1;
+          const float s = sx[j] * (h ? swb[j] : swa[j]);
           const float2 s2 = make_float2(s, s);
-          uint32_t v[2][16];
-          tmem_ld16(tb, v[0]);
+          uint32_t ready = 0;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
+          for (int c = 0; c < 4; ++c) {
             tmem_ld_wait();
             tmem_regs_ready(v[c & 1]);
-            if (c < 7) {
+            if (c < 3) {
               tmem_ld16(tb + 16 * (c + 1), v[(c + 1) & 1]);
             } else {
               tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&sm.acc_free[b]), 0));
+              mbar_arrive_if(lane == 0, free0 + 8 * b);
+              if (h == 0 || kb + 1 < p.G) {
+                if (!__all_sync(0xffffffffu, ready) && !warp_wait(&sm.acc_full[nb], npar, p.wait_ns, p.err)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
+                tmem_ld16(tq + UN * nb, v[0]);
+              }
+            }
+            if (c == 0) ready = mbar_try_wait_relaxed(&sm.acc_full[nb], npar);
+            if (h == 1 && c == 1) {
+              const int kn = min(kb + 2, p.G - 1);
+              sx[j] = __ldg(sxp + (size_t)kn * p.M);
+              swa[j] = __ldg(swp + kn);
+              swb[j] = __ldg(swp + sw1 + kn);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              acc[8 * c + i] = __ffma2_rn(
-                  make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), s2, acc[8 * c + i]);
+              acc[32 * h + 8 * c + i] =
+                  __ffma2_rn(make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), s2,
+                             acc[32 * h + 8 * c + i]);
           }
-          ++it;
+          if (!ok) break;
+          if (h == 1) ++it;
         }
       }
       if (!ok) break;
@@ -244,7 +278,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       if (p.out_f32) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int n = n0 + 32 * c;
+          const int n = n0 + 128 * (c >> 1) + 32 * (c & 1);
           uint8_t* buf = sm.out[e][c % kSlots];
           if (lane == 0) bulk_wait_read<kSlots - 1>();
           __syncwarp();
@@ -271,7 +305,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       } else {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int n = n0 + 64 * c;
+          const int n = n0 + 128 * c;
           uint8_t* buf = sm.out[e][c % kSlots];
           if (lane == 0) bulk_wait_read<kSlots - 1>();
           __syncwarp();
@@ -320,7 +354,7 @@ cudaError_t launch_fp8_linear(const Fp8GemmArgs& a, cudaStream_t s) {
   CUtensorMap tm_a, tm_b, tm_y;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
   bool ok = make_tmap_2d(&tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.x_codes, a.K, a.M, a.K, BK, BM, sw) &&
-            make_tmap_2d(&tm_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w_codes, a.K, a.N, a.K, BK, BN / 2, sw);
+            make_tmap_2d(&tm_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w_codes, a.K, a.N, a.K, BK, UN / 2, sw);
   if (a.out_f32)
     ok = ok && make_tmap_2d(&tm_y, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.y, a.N, a.M, (uint64_t)a.N * 4, 32, 32, sw);
   else
