@@ -76,6 +76,13 @@ __device__ __forceinline__ bool mbar_wait_relaxed(uint64_t* bar, uint32_t parity
   }
 }
 
+// two fp32 -> bf16x2 (round to nearest even); `lo` in bits 0..15
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // Register shares of a warpgroup (all four warps execute it).
 template <int N>
 __device__ __forceinline__ void regs_inc() {

@@ -320,7 +320,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
                 a.x += bf16_bits_to_f32(bw & 0xFFFFu);
                 a.y += bf16_bits_to_f32(bw >> 16);
               }
-              w4[k] = f32_to_bf16_bits(a.x) | (f32_to_bf16_bits(a.y) << 16);
+              w4[k] = pack_bf16x2(a.x, a.y);
             }
             *reinterpret_cast<uint4*>(buf + lane * 128 + ((u ^ (lane & 7)) * 16)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
           }
@@ -351,6 +351,8 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
 }  // namespace
 
 cudaError_t launch_fp8_linear(const Fp8GemmArgs& a, cudaStream_t s) {
+  int tokens, split;
+  if (fp8_rows_plan(a, &tokens, &split)) return launch_fp8_rows(a, tokens, split, s);
   CUtensorMap tm_a, tm_b, tm_y;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
   bool ok = make_tmap_2d(&tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.x_codes, a.K, a.M, a.K, BK, BM, sw) &&

@@ -1,0 +1,320 @@
+// The 8-bit GEMM (svdq_fp8_linear) for few rows: one token of a decoding
+// step up to a few hundred. It reads every weight once, so it is bound by HBM
+// (N K bytes) until the rows' products take longer than the weights' way in.
+//
+// The operands change places: 128 weight rows are the M of a tcgen05.mma, T
+// tokens (16 .. 128) its N, so a handful of tokens fills the tensor cores as
+// well as it can. One CTA has a 128-column x T-token tile of y and a part of K;
+// the CTAs of a cluster share the tile and split K (S of them), so that few
+// column tiles still keep all SMs reading. At the end every CTA sends its
+// partial sums of token t to CTA t mod S of its cluster, which adds them in
+// the order of the ranks (the result does not depend on timing), adds the bias
+// and rounds once.
+//
+//   warp 0      TMA producer: per K block the 128 x 128 weight tile and the
+//               T x 128 activation tile, 128B-swizzled
+//   warp 1      tensor memory, MMA issuer: per block one product into one of
+//               kBufs accumulators
+//   warps 2..5  drain: a thread is a weight row; per block T sums, each times
+//               its token's scale (the block's weight scale multiplied in when
+//               the scales are brought into shared memory, ahead of the loop)
+#include "fp8.cuh"
+#include "kernels.h"
+
+namespace svdq {
+namespace {
+
+constexpr int kThreadsR = 192;
+constexpr int kMaxSplit = 8;           // portable cluster size
+
+template <int T>
+struct CfgR {
+  static constexpr int kWBytes = 128 * 128, kXBytes = T * 128;
+  static constexpr int kStageBytes = kWBytes + kXBytes;
+  static constexpr int kBufs = T > 64 ? 2 : 4;
+  static constexpr uint32_t kTmemCols = T * kBufs < 32 ? 32 : T * kBufs;
+  static constexpr int kCtas = T <= 32 ? 2 : 1;   // CTAs per SM
+  static constexpr int kScaleFloats = T <= 32 ? 4096 : 8192;   // scales of a CTA's part of K: blocks x T
+  static constexpr int kRedBytes = T * 128 * 4;
+  static constexpr int kFixed = kScaleFloats * 4 + kRedBytes + 512 + 1024;
+  static constexpr int kFit = ((T <= 32 ? 113 : 226) * 1024 - kFixed) / kStageBytes;
+  static constexpr int kStages = kFit > 8 ? 8 : kFit;
+  static constexpr int kSmem = kFixed + kStages * kStageBytes;
+};
+
+struct ParamsR {
+  const float* x_scales;
+  const float* w_scales;
+  const uint16_t* bias;
+  void* y;
+  int M, N, G, split;
+  int out_f32;
+  unsigned* err;
+  unsigned long long wait_ns;
+};
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+template <int T>
+__global__ void __launch_bounds__(kThreadsR, CfgR<T>::kCtas)
+gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                     const ParamsR p) {
+  using C = CfgR<T>;
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* stages = smem_align<1024>(smem_raw);
+  float* scl = reinterpret_cast<float*>(stages + S * C::kStageBytes);   // [blocks][T]
+  float* red = scl + C::kScaleFloats;                                     // [split][T / split][128]
+  uint64_t* full = reinterpret_cast<uint64_t*>(red + T * 128);
+  uint64_t* empty = full + S;
+  uint64_t* acc_full = empty + S;
+  uint64_t* acc_free = acc_full + C::kBufs;
+  uint64_t* mma_done = acc_free + C::kBufs;
+  uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(mma_done + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)blockIdx.x % p.split, tn = (int)blockIdx.x / p.split;
+  const int n0 = tn * 128, m0 = (int)blockIdx.y * T;
+  const int kb0 = (int)((long long)p.G * rank / p.split), kb1 = (int)((long long)p.G * (rank + 1) / p.split);
+  const int nkb = kb1 - kb0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < C::kBufs; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_free[b], 4);
+    }
+    mbar_init(mma_done, 1);
+    fence_mbar_init();
+    // weights are hardly ever the previous kernel's output: their way to L2
+    // may begin before it ends (a prefetch only moves data closer)
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_x);
+    for (int k = 0; k < nkb && k < S; ++k) tma_prefetch_l2_2d(&tm_w, (kb0 + k) * 128, n0);
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tmem_alloc(tmem_ptr, C::kTmemCols);
+    tmem_relinquish();
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_ptr;
+  // (its wait, ahead of the first write to another CTA's shared memory, tells
+  // that every CTA of the cluster has started)
+  cluster_arrive();
+  // every input may be the previous kernel's output, y may still be read by it
+  if (threadIdx.x == 0) launch_dependents();
+  grid_dependency_wait();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int k = 0;
+      bool ok = true;
+      for (; k < nkb; ++k) {
+        const int s = k % S;
+        if (k >= S && !mbar_wait(&empty[s], ((k / S) - 1) & 1, p.wait_ns, p.err)) { ok = false; break; }
+        uint8_t* st = stages + s * C::kStageBytes;
+        mbar_expect_tx(&full[s], C::kStageBytes);
+        tma_load_2d(st, &tm_w, &full[s], (kb0 + k) * 128, n0);
+        tma_load_2d(st + C::kWBytes, &tm_x, &full[s], (kb0 + k) * 128, m0);
+      }
+      if (!ok) {
+        // let the copies already issued land before the CTA can exit
+        for (int j = max(0, k - S); j < k; ++j) (void)mbar_wait(&full[j % S], (j / S) & 1, p.wait_ns, nullptr);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    for (int k = 0; k < nkb; ++k) {
+      const int s = k % S, b = k % C::kBufs;
+      if (!warp_wait(&full[s], (k / S) & 1, p.wait_ns, p.err)) break;
+      if (!warp_wait(&acc_free[b], ((k / C::kBufs) & 1) ^ 1, p.wait_ns, p.err)) break;
+      tc_fence_after();
+      const uint32_t st = smem_u32(stages + s * C::kStageBytes);
+      const uint64_t da = make_sdesc(st, 16, 1024, kLayoutSw128);
+      const uint64_t db = make_sdesc(st + C::kWBytes, 16, 1024, kLayoutSw128);
+      if (elect_one()) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma_f8(tmem + T * b, da + 2 * j, db + 2 * j, f8_idesc(128, T), j > 0 ? 1u : 0u);
+        tc_commit(&acc_full[b]);
+        tc_commit(&empty[s]);
+      }
+      __syncwarp();
+    }
+    // every MMA issued has completed before tensor memory is freed
+    if (elect_one()) tc_commit(mma_done);
+    __syncwarp();
+    (void)warp_wait(mma_done, 0, p.wait_ns, p.err);
+  }
+
+  const int tv = min(T, p.M - m0);   // tokens of the tile
+  float2 acc[T / 2];
+  if (warp >= 2) {
+    // ------------------------------------------------------------ drain
+    const int dt = threadIdx.x - 64;
+    const float* swp = p.w_scales + (size_t)tn * p.G;
+    for (int i = dt; i < nkb * T; i += 128) {
+      const int k = i / T, t = i % T;
+      scl[i] = t < tv ? __ldg(p.x_scales + (size_t)(kb0 + k) * p.M + m0 + t) * __ldg(swp + kb0 + k) : 0.f;
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < T / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+    const uint32_t tq = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    for (int k = 0; k < nkb; ++k) {
+      const int b = k % C::kBufs;
+      if (!warp_wait(&acc_full[b], (k / C::kBufs) & 1, p.wait_ns, p.err)) break;
+      tc_fence_after();
+      const float4* sv = reinterpret_cast<const float4*>(scl + k * T);
+#pragma unroll
+      for (int c = 0; c < T / 16; ++c) {
+        uint32_t v[16];
+        tmem_ld16(tq + T * b + 16 * c, v);
+        tmem_ld_wait();
+        tmem_regs_ready(v);
+        if (c == T / 16 - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_free[b]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 s = sv[4 * c + i];
+          acc[8 * c + 2 * i] = __ffma2_rn(make_float2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])),
+                                          make_float2(s.x, s.y), acc[8 * c + 2 * i]);
+          acc[8 * c + 2 * i + 1] = __ffma2_rn(make_float2(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])),
+                                              make_float2(s.z, s.w), acc[8 * c + 2 * i + 1]);
+        }
+      }
+    }
+  }
+
+  // ---------------------------------------------------------------- output
+  const int r = 32 * (warp & 3) + lane, n = n0 + r;   // drain threads: weight row of the tile, column of y
+  const float bias = warp >= 2 && n < p.N && p.bias ? bf16_bits_to_f32(p.bias[n]) : 0.f;
+  auto put = [&](int t, float v) {
+    const size_t at = (size_t)(m0 + t) * p.N + n;
+    if (p.out_f32)
+      static_cast<float*>(p.y)[at] = v + bias;
+    else
+      static_cast<uint16_t*>(p.y)[at] = (uint16_t)f32_to_bf16_bits(v + bias);
+  };
+  if (p.split == 1) {
+    if (warp >= 2 && n < p.N) {
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+        if (t < tv) put(t, t & 1 ? acc[t / 2].y : acc[t / 2].x);
+    }
+  }
+  __syncwarp();
+  cluster_wait();
+  if (p.split > 1) {
+    const int per = T / p.split;   // tokens a CTA may have to add
+    if (warp >= 2) {
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+        if (t < tv) {
+          const uint32_t at = smem_u32(red + ((size_t)rank * per + t / p.split) * 128 + r);
+          st_cluster_f32(mapa_shared(at, (uint32_t)(t % p.split)), t & 1 ? acc[t / 2].y : acc[t / 2].x);
+        }
+    }
+    __syncwarp();
+    cluster_sync();
+    if (warp >= 2 && n < p.N) {
+      for (int t = rank; t < tv; t += p.split) {
+        float v = 0.f;
+        for (int i = 0; i < p.split; ++i) v += red[((size_t)i * per + t / p.split) * 128 + r];
+        put(t, v);
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+template <int T>
+cudaError_t launch_rows_t(const Fp8GemmArgs& a, int split, cudaStream_t s) {
+  using C = CfgR<T>;
+  static_assert(C::kStages >= 3 && (2 * C::kStages + 2 * C::kBufs + 2) * 8 <= 512, "shared-memory plan");
+  CUtensorMap tm_w, tm_x;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  if (!make_tmap_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w_codes, a.K, a.N, a.K, 128, 128, sw) ||
+      !make_tmap_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.x_codes, a.K, a.M, a.K, 128, T, sw))
+    return cudaErrorInvalidValue;
+  ParamsR p;
+  p.x_scales = a.x_scales;
+  p.w_scales = a.w_scales;
+  p.bias = a.bias;
+  p.y = a.y;
+  p.M = a.M; p.N = a.N;
+  p.G = (a.K + 127) / 128;
+  p.split = split;
+  p.out_f32 = a.out_f32;
+  p.err = a.err;
+  p.wait_ns = a.wait_ns;
+  auto kern = gemm_fp8_rows_kernel<T>;
+  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), C::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.N + 127) / 128 * split), (unsigned)((a.M + T - 1) / T));
+  cfg.blockDim = dim3(kThreadsR);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, kern, tm_w, tm_x, p);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool fp8_rows_plan(const Fp8GemmArgs& a, int* tokens, int* split) {
+  const int M = a.M, K = a.K, N = a.N, num_sms = a.num_sms;
+  if (M > 32) return false;
+  const int G = (K + 127) / 128;
+  const int T = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  const int tiles = (N + 127) / 128 * ((M + T - 1) / T);
+  int S = 1;
+  while (S < kMaxSplit && 2 * S <= G && tiles * S < num_sms) S *= 2;
+  if ((G + S - 1) / S * T > (T <= 32 ? CfgR<16>::kScaleFloats : CfgR<64>::kScaleFloats)) return false;
+  *tokens = T;
+  *split = S;
+  return true;
+}
+
+cudaError_t launch_fp8_rows(const Fp8GemmArgs& a, int tokens, int split, cudaStream_t s) {
+  switch (tokens) {
+    case 16: return launch_rows_t<16>(a, split, s);
+    case 32: return launch_rows_t<32>(a, split, s);
+    case 64: return launch_rows_t<64>(a, split, s);
+    default: return launch_rows_t<128>(a, split, s);
+  }
+}
+
+}  // namespace svdq

@@ -135,6 +135,10 @@ struct Fp8GemmArgs {
   int num_sms;
 };
 cudaError_t launch_fp8_linear(const Fp8GemmArgs& a, cudaStream_t s);
+// few rows (gemm_fp8_rows.cu): whether that kernel is taken, and with which
+// token tile and split of K; launch_fp8_linear dispatches to it
+bool fp8_rows_plan(const Fp8GemmArgs& a, int* tokens, int* split);
+cudaError_t launch_fp8_rows(const Fp8GemmArgs& a, int tokens, int split, cudaStream_t s);
 
 constexpr int kRopeMaxPairs = 512;
 struct RopeArgs {
