@@ -15,7 +15,8 @@
 //               T x 128 activation tile, 128B-swizzled
 //   warp 1      tensor memory, MMA issuer: per block one product into one of
 //               kBufs accumulators
-//   warps 2..5  drain: a thread is a weight row; per block T sums, each times
+//   others      drain, one warp per lane quadrant (two, with half the tokens
+//               each, above 32): a thread is a weight row; its sums, each times
 //               its token's scale (the block's weight scale multiplied in when
 //               the scales are brought into shared memory, ahead of the loop)
 #include "fp8.cuh"
@@ -24,18 +25,21 @@
 namespace svdq {
 namespace {
 
-constexpr int kThreadsR = 192;
 constexpr int kMaxSplit = 8;           // portable cluster size
 
 template <int T>
 struct CfgR {
+  static constexpr int kDrainWarps = T > 32 ? 8 : 4;
+  static constexpr int kThreads = 64 + 32 * kDrainWarps;
+  static constexpr int kHT = T / (kDrainWarps / 4);   // tokens of a drain thread
   static constexpr int kWBytes = 128 * 128, kXBytes = T * 128;
   static constexpr int kStageBytes = kWBytes + kXBytes;
   static constexpr int kBufs = T > 64 ? 2 : 4;
   static constexpr uint32_t kTmemCols = T * kBufs < 32 ? 32 : T * kBufs;
   static constexpr int kCtas = T <= 32 ? 2 : 1;   // CTAs per SM
   static constexpr int kScaleFloats = T <= 32 ? 4096 : 8192;   // scales of a CTA's part of K: blocks x T
-  static constexpr int kRedBytes = T * 128 * 4;
+  // partial sums: split x the tokens a CTA adds (at least 4) x 128 rows
+  static constexpr int kRedBytes = (T > 4 * kMaxSplit ? T : 4 * kMaxSplit) * 128 * 4;
   static constexpr int kFixed = kScaleFloats * 4 + kRedBytes + 512 + 1024;
   static constexpr int kFit = ((T <= 32 ? 113 : 226) * 1024 - kFixed) / kStageBytes;
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
@@ -55,12 +59,12 @@ struct ParamsR {
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+__device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
 
 template <int T>
-__global__ void __launch_bounds__(kThreadsR, CfgR<T>::kCtas)
+__global__ void __launch_bounds__(CfgR<T>::kThreads, CfgR<T>::kCtas)
 gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                      const ParamsR p) {
   using C = CfgR<T>;
@@ -68,8 +72,8 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = smem_align<1024>(smem_raw);
   float* scl = reinterpret_cast<float*>(stages + S * C::kStageBytes);   // [blocks][T]
-  float* red = scl + C::kScaleFloats;                                     // [split][T / split][128]
-  uint64_t* full = reinterpret_cast<uint64_t*>(red + T * 128);
+  float* red = scl + C::kScaleFloats;                                     // [split][tokens / 4][128][4]
+  uint64_t* full = reinterpret_cast<uint64_t*>(red + C::kRedBytes / 4);
   uint64_t* empty = full + S;
   uint64_t* acc_full = empty + S;
   uint64_t* acc_free = acc_full + C::kBufs;
@@ -89,7 +93,7 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
     }
     for (int b = 0; b < C::kBufs; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_free[b], 4);
+      mbar_init(&acc_free[b], C::kDrainWarps);
     }
     mbar_init(mma_done, 1);
     fence_mbar_init();
@@ -137,14 +141,21 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
+    // descriptors of stage 0; a stage further is kStageBytes further, a K
+    // step of 32 bytes 2 (addresses are in units of 16 bytes)
+    const uint64_t a0 = make_sdesc(smem_u32(stages), 16, 1024, kLayoutSw128);
+    const uint64_t b0 = make_sdesc(smem_u32(stages) + C::kWBytes, 16, 1024, kLayoutSw128);
+    uint32_t s = 0, sph = 0, b = 0, bph = 1;
     for (int k = 0; k < nkb; ++k) {
-      const int s = k % S, b = k % C::kBufs;
-      if (!warp_wait(&full[s], (k / S) & 1, p.wait_ns, p.err)) break;
-      if (!warp_wait(&acc_free[b], ((k / C::kBufs) & 1) ^ 1, p.wait_ns, p.err)) break;
+      // both barriers tested at once: the tests' latencies are a good part of
+      // a block's time here
+      const bool rf = mbar_try_wait(&acc_free[b], bph);
+      const bool rs = mbar_try_wait(&full[s], sph);
+      if (!__all_sync(0xffffffffu, rs && rf) && !(warp_wait(&full[s], sph, p.wait_ns, p.err) &&
+                                                  warp_wait(&acc_free[b], bph, p.wait_ns, p.err)))
+        break;
       tc_fence_after();
-      const uint32_t st = smem_u32(stages + s * C::kStageBytes);
-      const uint64_t da = make_sdesc(st, 16, 1024, kLayoutSw128);
-      const uint64_t db = make_sdesc(st + C::kWBytes, 16, 1024, kLayoutSw128);
+      const uint64_t da = a0 + (uint64_t)(s * (C::kStageBytes >> 4)), db = b0 + (uint64_t)(s * (C::kStageBytes >> 4));
       if (elect_one()) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) mma_f8(tmem + T * b, da + 2 * j, db + 2 * j, f8_idesc(128, T), j > 0 ? 1u : 0u);
@@ -152,6 +163,14 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
         tc_commit(&empty[s]);
       }
       __syncwarp();
+      if (++s == (uint32_t)S) {
+        s = 0;
+        sph ^= 1;
+      }
+      if (++b == (uint32_t)C::kBufs) {
+        b = 0;
+        bph ^= 1;
+      }
     }
     // every MMA issued has completed before tensor memory is freed
     if (elect_one()) tc_commit(mma_done);
@@ -159,32 +178,48 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
     (void)warp_wait(mma_done, 0, p.wait_ns, p.err);
   }
 
-  const int tv = min(T, p.M - m0);   // tokens of the tile
-  float2 acc[T / 2];
+  const int tv = min(T, p.M - m0);            // tokens of the tile
+  constexpr int HT = C::kHT;
+  const int t0 = (warp - 2) / 4 * HT;         // this drain warp's tokens
+  float2 acc[HT / 2];
   if (warp >= 2) {
     // ------------------------------------------------------------ drain
+    constexpr int kD = 32 * C::kDrainWarps;
     const int dt = threadIdx.x - 64;
-    const float* swp = p.w_scales + (size_t)tn * p.G;
-    for (int i = dt; i < nkb * T; i += 128) {
-      const int k = i / T, t = i % T;
-      scl[i] = t < tv ? __ldg(p.x_scales + (size_t)(kb0 + k) * p.M + m0 + t) * __ldg(swp + kb0 + k) : 0.f;
-    }
-    asm volatile("bar.sync 1, 128;" ::: "memory");
+    const float* swp = p.w_scales + (size_t)tn * p.G + kb0;
+    const float* sxp = p.x_scales + (size_t)kb0 * p.M + m0;
+    // eight loads of each kind in flight
+    for (int i0 = dt; i0 < nkb * T; i0 += 8 * kD) {
+      float a[8], b[8];
 #pragma unroll
-    for (int i = 0; i < T / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-    const uint32_t tq = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * kD, k = i / T, t = i % T;
+        const bool in = k < nkb && t < tv;
+        a[u] = in ? __ldg(sxp + (size_t)k * p.M + t) : 0.f;
+        b[u] = in ? __ldg(swp + k) : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (i0 + u * kD < nkb * T) scl[i0 + u * kD] = a[u] * b[u];
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(kD) : "memory");
+#pragma unroll
+    for (int i = 0; i < HT / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+    const uint32_t tq = tmem + t0 + ((uint32_t)(32 * (warp & 3)) << 16);
     for (int k = 0; k < nkb; ++k) {
       const int b = k % C::kBufs;
       if (!warp_wait(&acc_full[b], (k / C::kBufs) & 1, p.wait_ns, p.err)) break;
       tc_fence_after();
-      const float4* sv = reinterpret_cast<const float4*>(scl + k * T);
+      const float4* sv = reinterpret_cast<const float4*>(scl + k * T + t0);
+      uint32_t v[2][16];
+      tmem_ld16(tq + T * b, v[0]);
 #pragma unroll
-      for (int c = 0; c < T / 16; ++c) {
-        uint32_t v[16];
-        tmem_ld16(tq + T * b + 16 * c, v);
+      for (int c = 0; c < HT / 16; ++c) {
         tmem_ld_wait();
-        tmem_regs_ready(v);
-        if (c == T / 16 - 1) {
+        tmem_regs_ready(v[c & 1]);
+        if (c + 1 < HT / 16) {
+          tmem_ld16(tq + T * b + 16 * (c + 1), v[(c + 1) & 1]);
+        } else {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&acc_free[b]);
@@ -192,9 +227,10 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float4 s = sv[4 * c + i];
-          acc[8 * c + 2 * i] = __ffma2_rn(make_float2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])),
+          const uint32_t* w = v[c & 1] + 4 * i;
+          acc[8 * c + 2 * i] = __ffma2_rn(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])),
                                           make_float2(s.x, s.y), acc[8 * c + 2 * i]);
-          acc[8 * c + 2 * i + 1] = __ffma2_rn(make_float2(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])),
+          acc[8 * c + 2 * i + 1] = __ffma2_rn(make_float2(__uint_as_float(w[2]), __uint_as_float(w[3])),
                                               make_float2(s.z, s.w), acc[8 * c + 2 * i + 1]);
         }
       }
@@ -214,29 +250,39 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
   if (p.split == 1) {
     if (warp >= 2 && n < p.N) {
 #pragma unroll
-      for (int t = 0; t < T; ++t)
-        if (t < tv) put(t, t & 1 ? acc[t / 2].y : acc[t / 2].x);
+      for (int t = 0; t < HT; ++t)
+        if (t0 + t < tv) put(t0 + t, t & 1 ? acc[t / 2].y : acc[t / 2].x);
     }
   }
   __syncwarp();
   cluster_wait();
   if (p.split > 1) {
-    const int per = T / p.split;   // tokens a CTA may have to add
+    // CTA j of the cluster adds tokens j * per .. of the tile
+    const int per = max(T / p.split, 4), owners = (tv + per - 1) / per;
     if (warp >= 2) {
 #pragma unroll
-      for (int t = 0; t < T; ++t)
-        if (t < tv) {
-          const uint32_t at = smem_u32(red + ((size_t)rank * per + t / p.split) * 128 + r);
-          st_cluster_f32(mapa_shared(at, (uint32_t)(t % p.split)), t & 1 ? acc[t / 2].y : acc[t / 2].x);
+      for (int t = 0; t < HT; t += 4)
+        if (t0 + t < tv) {
+          const int to = (t0 + t) / per, at = (t0 + t) % per / 4;
+          st_cluster_f32x4(mapa_shared(smem_u32(red + ((rank * (per / 4) + at) * 128 + r) * 4), (uint32_t)to),
+                           acc[t / 2].x, acc[t / 2].y, acc[t / 2 + 1].x, acc[t / 2 + 1].y);
         }
     }
     __syncwarp();
     cluster_sync();
-    if (warp >= 2 && n < p.N) {
-      for (int t = rank; t < tv; t += p.split) {
-        float v = 0.f;
-        for (int i = 0; i < p.split; ++i) v += red[((size_t)i * per + t / p.split) * 128 + r];
-        put(t, v);
+    if (warp >= 2 && n < p.N && rank < owners) {
+      for (int u = (warp - 2) / 4; u < per / 4; u += C::kDrainWarps / 4) {
+        const int t = rank * per + 4 * u;
+        if (t >= tv) break;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < p.split; ++i) {
+          const float4 w = *reinterpret_cast<const float4*>(red + ((i * (per / 4) + u) * 128 + r) * 4);
+          v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+        }
+        put(t, v.x);
+        if (t + 1 < tv) put(t + 1, v.y);
+        if (t + 2 < tv) put(t + 2, v.z);
+        if (t + 3 < tv) put(t + 3, v.w);
       }
     }
   }
@@ -275,7 +321,7 @@ cudaError_t launch_rows_t(const Fp8GemmArgs& a, int split, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((a.N + 127) / 128 * split), (unsigned)((a.M + T - 1) / T));
-  cfg.blockDim = dim3(kThreadsR);
+  cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
