@@ -340,18 +340,52 @@ cudaError_t launch_rows_t(const Fp8GemmArgs& a, int split, cudaStream_t s) {
 
 }  // namespace
 
+// The plan is the one with the least estimated time, in microseconds:
+//   this kernel     waves (a + c blocks) + 1.2 with a split
+//   the pair kernel 6.5 + waves (2 + 0.44 blocks)
+// where a wave is one CTA (pair) per SM and blocks the K blocks of a CTA.
+// Measured at N = 4096 with 8, 32 and 64 blocks: T = 64 5.9, 12.3, 20.7 us
+// (a = 3.8, c = 0.265), T = 128 8.0, 15.6, 26.4 (5.4, 0.33), the pair kernel
+// 12.6, 23.4, 37.3; three waves of it at 32 blocks 54.4. So M = 512, N = K =
+// 4096 comes here (16.6 us against 23.9), M = 512 with N = 12288 does not.
+// Up to 32 tokens the tile is as wide as they are and two CTAs fit on an SM,
+// but the second set is better left to the next launch, whose start it hides
+// (1 x 4096 x 9216: 144 CTAs 9.0 us, 288 11.9), unless a CTA's part of K is
+// long (16 x 12288 x 4096: 12 blocks on 256 CTAs 10.6 us, 24 on 128 11.9;
+// 1 x 4096 x 18432: 16 on 288 13.7, 32 on 144 15.1).
+// Clusters of 8 find room on about half of the SMs at one CTA each
+// (64 x 1024 x 2048: 8.5 us against 4.5 with clusters of 4).
 bool fp8_rows_plan(const Fp8GemmArgs& a, int* tokens, int* split) {
-  const int M = a.M, K = a.K, N = a.N, num_sms = a.num_sms;
-  if (M > 32) return false;
-  const int G = (K + 127) / 128;
-  const int T = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-  const int tiles = (N + 127) / 128 * ((M + T - 1) / T);
-  int S = 1;
-  while (S < kMaxSplit && 2 * S <= G && tiles * S < num_sms) S *= 2;
-  if ((G + S - 1) / S * T > (T <= 32 ? CfgR<16>::kScaleFloats : CfgR<64>::kScaleFloats)) return false;
-  *tokens = T;
-  *split = S;
-  return true;
+  const int G = (a.K + 127) / 128;
+  const long long tn = (a.N + 127) / 128;
+  auto up = [](long long x, long long y) { return (x + y - 1) / y; };
+  if (a.M <= 32) {
+    const int T = a.M <= 16 ? 16 : 32;
+    int S = 1;
+    while (S < kMaxSplit && 2 * S <= G && 2 * S * tn <= a.num_sms) S *= 2;
+    if (S < kMaxSplit && up(G, S) >= 24 && 2 * S * tn <= 2 * a.num_sms) S *= 2;
+    if (up(G, S) * T > CfgR<16>::kScaleFloats) return false;
+    *tokens = T;
+    *split = S;
+    return true;
+  }
+  const double pair = 6.5 + (double)up(up(a.M, 256) * up(a.N, 256), a.num_sms / 2) * (2.0 + 0.44 * G);
+  double best = pair;
+  for (int T : {64, 128}) {
+    const long long tiles = tn * up(a.M, T);
+    for (int S = 1; S <= kMaxSplit && S <= G; S *= 2) {
+      if (S == 8 && tiles * S > a.num_sms / 2) break;
+      if (up(G, S) * T > CfgR<64>::kScaleFloats || up(a.M, T) > 65535) continue;
+      const double blocks = (double)up(G, S), waves = (double)up(tiles * S, a.num_sms);
+      const double t = waves * (T == 64 ? 3.8 + 0.265 * blocks : 5.4 + 0.33 * blocks) + (S > 1 ? 1.2 : 0.0);
+      if (t < best) {
+        best = t;
+        *tokens = T;
+        *split = S;
+      }
+    }
+  }
+  return best < pair;
 }
 
 cudaError_t launch_fp8_rows(const Fp8GemmArgs& a, int tokens, int split, cudaStream_t s) {
