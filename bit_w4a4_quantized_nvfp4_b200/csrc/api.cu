@@ -436,9 +436,10 @@ svdq_status svdq_fp8_quantize_act(int M, int K, const uint16_t* x, long long ldx
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return SVDQ_ERR_ALIGN;
   const Span sx = rows_span(x, M, K, ldx, 2), sc = span(codes, (size_t)M * K), ss = fp8_scale_span(scales, M, K);
   if (overlap(sc, sx) || overlap(ss, sx) || overlap(sc, ss)) return SVDQ_ERR_INVALID_ARG;
-  if ((st = device_info(nullptr, nullptr)) != SVDQ_OK) return st;
+  int sms = 0;
+  if ((st = device_info(nullptr, &sms)) != SVDQ_OK) return st;
   Fp8ActArgs a{x, nullptr, nullptr, nullptr, codes, scales, ldx, 0, 0, M, K, 0.f};
-  return from_cuda(launch_fp8_act(a, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_fp8_act(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 svdq_status svdq_fp8_norm_quantize(int M, int K, const uint16_t* x, long long ldx, const uint16_t* residual,
@@ -466,9 +467,10 @@ svdq_status svdq_fp8_norm_quantize(int M, int K, const uint16_t* x, long long ld
     if (overlap(so, sx) && !(residual_out == x && ldo == ldx)) return SVDQ_ERR_INVALID_ARG;
     if (overlap(so, sr) && !(residual_out == residual && ldo == ldr)) return SVDQ_ERR_INVALID_ARG;
   }
-  if ((st = device_info(nullptr, nullptr)) != SVDQ_OK) return st;
+  int sms = 0;
+  if ((st = device_info(nullptr, &sms)) != SVDQ_OK) return st;
   Fp8ActArgs a{x, residual, weight, residual_out, codes, scales, ldx, ldr, ldo, M, K, eps};
-  return from_cuda(launch_fp8_act(a, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_fp8_act(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 svdq_status svdq_fp8_pack_weight(int K, int N, const float* W, uint8_t* codes, float* scales, void* stream) {

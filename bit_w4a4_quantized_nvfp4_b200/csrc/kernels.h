@@ -116,7 +116,7 @@ struct Fp8ActArgs {
   float eps;
 };
 constexpr int kFp8NormMaxK = 32768;
-cudaError_t launch_fp8_act(const Fp8ActArgs& a, cudaStream_t s);
+cudaError_t launch_fp8_act(const Fp8ActArgs& a, int num_sms, cudaStream_t s);
 
 // W [K, N] -> codes [N, K], scales [ceil(N/128), ceil(K/128)]
 cudaError_t launch_fp8_pack(int K, int N, const float* W, uint8_t* codes, float* scales, cudaStream_t s);
