@@ -11,176 +11,189 @@
 // twice); the residual's sum is rounded to bf16 first, since that is the
 // value the next layer reads.
 //
-// Norm: a row belongs to tpr threads (a power of two of warps) and stays in
-// their registers; CTAs are persistent, hold the norm weight in registers
-// and load their next row while the current one is reduced. Without the norm
-// blocks are independent: a warp takes four pieces of 256 columns at a time.
+// Norm: one pass, a row to a warp (to several while rows are few). Without the
+// norm blocks are independent: a warp takes four pieces of 256 columns at a
+// time.
 #include "fp8.cuh"
 #include "kernels.h"
 
 namespace svdq {
 namespace {
 
-// largest magnitude of 8 values; a NaN among them stays
-__device__ __forceinline__ float absmax8(const float (&v)[8]) {
-  float a = max_nan(fabsf(v[0]), fabsf(v[1])), b = max_nan(fabsf(v[2]), fabsf(v[3]));
-  const float c = max_nan(fabsf(v[4]), fabsf(v[5])), d = max_nan(fabsf(v[6]), fabsf(v[7]));
-  a = max_nan(a, b);
-  b = max_nan(c, d);
-  return max_nan(a, b);
+// largest magnitude of three / of 8 values; a NaN among them stays
+__device__ __forceinline__ float absmax3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float absmax8(const float2 (&v)[4]) {
+  return absmax3(absmax3(v[0].x, v[0].y, v[1].x), absmax3(v[1].y, v[2].x, v[2].y), absmax3(v[3].x, v[3].y, 0.f));
 }
 
-// the same over the 16 lanes of a block, and the block's scale
-__device__ __forceinline__ float block_scale(float am) {
+// the same over the 16 lanes of a block (`lanes`: those that take part)
+__device__ __forceinline__ float block_max(float am, unsigned lanes = 0xffffffffu) {
 #pragma unroll
-  for (int o = 8; o; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
-  return max_nan(am * (1.0f / 448.0f), kFp8MinScale);
+  for (int o = 8; o; o >>= 1) am = max_nan(am, __shfl_xor_sync(lanes, am, o));
+  return am;
 }
+__device__ __forceinline__ float scale_of(float am) { return max_nan(am * (1.0f / 448.0f), kFp8MinScale); }
 
-// 8 codes of v / scale (as v times the rounded reciprocal: half a step of
-// fp32 more, against half a step of E4M3)
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float rcp) {
-  uint2 r;
-  asm("{\n\t.reg .b16 a, b;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
-      "mov.b32 %0, {a, b};\n\t}"
-      : "=r"(r.x)
-      : "f"(v[0] * rcp), "f"(v[1] * rcp), "f"(v[2] * rcp), "f"(v[3] * rcp));
-  asm("{\n\t.reg .b16 a, b;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
-      "mov.b32 %0, {a, b};\n\t}"
-      : "=r"(r.y)
-      : "f"(v[4] * rcp), "f"(v[5] * rcp), "f"(v[6] * rcp), "f"(v[7] * rcp));
+__device__ __forceinline__ float rcp(float v) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
 
-__device__ __forceinline__ void unpack8(const uint4 q, float (&v)[8]) {
+// 8 codes of v * f. f is a rounded reciprocal, which with the product is off
+// by under 2^-22, against half a step of E4M3, 2^-4.
+__device__ __forceinline__ uint2 codes8(const float2 (&v)[4], float f) {
+  uint32_t r[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float2 a = __fmul2_rn(v[2 * h], make_float2(f, f)), b = __fmul2_rn(v[2 * h + 1], make_float2(f, f));
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
+        "mov.b32 %0, {a, b};\n\t}"
+        : "=r"(r[h])
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  }
+  return make_uint2(r[0], r[1]);
+}
+
+__device__ __forceinline__ void unpack8(const uint4 q, float2 (&v)[4]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
 
 // ------------------------------------------------------------------ norm
-constexpr int kMaxWarps = 16;
-
-template <int VPT, bool RES>
-__global__ void __launch_bounds__(512) fp8_norm_kernel(const Fp8ActArgs a, int tpr) {
-  __shared__ float part[2][kMaxWarps];
+// A block's codes do not depend on the row's norm: with t = r w the block's v
+// is t / rms, its largest magnitude max|t| / rms, and v / scale = 448 t /
+// max|t|. So one pass over the row writes r and the codes and leaves only
+// max|t| of each block behind; the scales follow once the row's sum is known,
+// and nothing of the row has to be held.
+// kAhead: vectors of 8 columns a thread has in flight (4, or as many as it has)
+template <bool RES, int kAhead>
+__global__ void __launch_bounds__(512, 2) fp8_norm_kernel(const Fp8ActArgs a, int wpr, float inv_k) {
+  __shared__ float part[2][16];
+  extern __shared__ float block_am[];   // [warps][2 * steps]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rpc = blockDim.x / tpr, mr = threadIdx.x / tpr, tid = threadIdx.x % tpr;
-  const int wpr = tpr / 32, w0 = mr * wpr;
-  const int nv = a.K / 8;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  const int mr = warp / wpr, w0 = mr * wpr, tpr = 32 * wpr;
+  const int tid = threadIdx.x - 32 * w0;
+  const int nv = a.K / 8, steps = (nv + tpr - 1) / tpr;
+  const long long m = (long long)blockIdx.x * ((blockDim.x >> 5) / wpr) + mr;
+  float* am_w = block_am + 2 * steps * warp;
   if (threadIdx.x == 0) launch_dependents();
   // every input may be the previous kernel's output, every output may still
   // be read by it
   grid_dependency_wait();
+  // (the last CTA's rows past M take the barriers below and write nothing)
+  const bool live = m < a.M;
+  const uint4* xp = reinterpret_cast<const uint4*>(a.x + (size_t)m * (size_t)a.ldx);
+  const uint4* qp = reinterpret_cast<const uint4*>(a.residual + (size_t)m * (size_t)a.ldr);
+  uint4* op = reinterpret_cast<uint4*>(a.residual_out + (size_t)m * (size_t)a.ldo);
+  const uint4* wp = reinterpret_cast<const uint4*>(a.weight);
+  uint2* cp = reinterpret_cast<uint2*>(a.codes + (size_t)m * a.K);
 
-  // registers for the weight and the next row: up to 4 vectors a thread
-  constexpr bool kAhead = VPT <= 4;
-  auto weight = [&](int j) {
-    const int i = j * tpr + tid;
-    return i < nv ? __ldg(reinterpret_cast<const uint4*>(a.weight) + i) : zero;
-  };
-  uint4 wv[VPT];
-  if (kAhead) {
+  float2 ss2 = make_float2(0.f, 0.f);
+  float least = 0x1p127f;   // the smallest max|t| of a block that is not all zeros
+  bool odd = false;         // a block whose products need the definition's order
+  for (int j0 = 0; j0 < steps; j0 += kAhead) {
+    uint4 r[kAhead], q[kAhead], w[kAhead];
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) wv[j] = weight(j);
-  }
-  // a barrier of the row's threads
-  auto row_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + mr), "r"(tpr) : "memory"); };
-  uint4 xn[VPT], rn[VPT];
-  auto fetch = [&](long long m) {
-    const uint4* xp = reinterpret_cast<const uint4*>(a.x + (size_t)m * (size_t)a.ldx);
-    const uint4* rp = reinterpret_cast<const uint4*>(a.residual + (size_t)m * (size_t)a.ldr);
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int i = j * tpr + tid;
-      const bool in = m < a.M && i < nv;
-      xn[j] = in ? xp[i] : zero;
-      if (RES) rn[j] = in ? rp[i] : zero;
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = (j0 + u) * tpr + tid;
+      const bool in = live && i < nv;
+      r[u] = in ? xp[i] : make_uint4(0u, 0u, 0u, 0u);
+      if (RES) q[u] = in ? qp[i] : make_uint4(0u, 0u, 0u, 0u);
+      w[u] = in ? __ldg(wp + i) : make_uint4(0u, 0u, 0u, 0u);
     }
-  };
-  const long long step = (long long)gridDim.x * rpc;
-  long long m = (long long)blockIdx.x * rpc + mr;
-  if (kAhead) fetch(m);
-  int par = 0;
-  for (long long base = (long long)blockIdx.x * rpc; base < a.M; base += step, m += step, par ^= 1) {
-    if (!kAhead) fetch(m);
-    uint4 r[VPT];
-    float ss = 0.f;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      float v[8];
-      unpack8(xn[j], v);
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = (j0 + u) * tpr + tid;
+      if (j0 + u >= steps) break;
+      float2 v[4], g[4];
+      unpack8(r[u], v);
       if (RES) {
-        float u[8];
-        unpack8(rn[j], u);
+        unpack8(q[u], g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += u[i];
-        r[j] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                          pack_bf16x2(v[6], v[7]));
-        unpack8(r[j], v);
-      } else {
-        r[j] = xn[j];
+        for (int k = 0; k < 4; ++k) v[k] = __fadd2_rn(v[k], g[k]);
+        r[u] = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
+                          pack_bf16x2(v[3].x, v[3].y));
+        unpack8(r[u], v);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-    }
-    if (RES && m < a.M) {
-      uint4* op = reinterpret_cast<uint4*>(a.residual_out + (size_t)m * (size_t)a.ldo);
+      for (int k = 0; k < 4; ++k) ss2 = __ffma2_rn(v[k], v[k], ss2);
+      unpack8(w[u], g);
 #pragma unroll
-      for (int j = 0; j < VPT; ++j)
-        if (j * tpr + tid < nv) op[j * tpr + tid] = r[j];
-    }
-    if (kAhead) fetch(m + step);
-    // the row's sum: lanes, then its warps in order (two buffers: a warp may
-    // be a row ahead of the slowest)
-    auto row_sum = [&](float s, float* buf) {
-#pragma unroll
-      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (wpr == 1) return s;
-      if (lane == 0) buf[warp] = s;
-      row_sync();
-      s = 0.f;
-      for (int i = 0; i < wpr; ++i) s += buf[w0 + i];
-      return s;
-    };
-    ss = row_sum(ss, part[par]);
-    float up = 1.f;
-    // squares of bf16 values can pass fp32's range at both ends: such a row is
-    // summed again, scaled by a power of two
-    if (ss > 0x1p120f || (ss < 0x1p-80f && a.eps < 0x1p-60f && m < a.M)) {
-      up = ss > 0x1p120f ? 0x1p-64f : 0x1p64f;
-      float s2 = 0.f;
-#pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        float v[8];
-        unpack8(r[j], v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s2 = fmaf(up * v[i], up * v[i], s2);
+      for (int k = 0; k < 4; ++k) v[k] = __fmul2_rn(v[k], g[k]);
+      const float am = block_max(absmax8(v));
+      const bool some = am != 0.f;
+      least = some ? fminf(least, am) : least;
+      odd = odd || (some && !(am >= 0x1p-100f && am < 0x1p127f));
+      const uint2 c = codes8(v, some ? 448.0f * rcp(am) : 0.f);
+      if (live && i < nv) {
+        if (RES) op[i] = r[u];
+        cp[i] = c;
       }
-      if (wpr > 1) row_sync();   // the first sums have been read
-      ss = row_sum(s2, part[par]);
+      if ((lane & 15) == 0) am_w[2 * (j0 + u) + (lane >> 4)] = am;
     }
-    const float inv = up * rsqrtf(ss / (float)a.K + up * up * a.eps);
+  }
+  // the row's sum: lanes, then its warps (the same order whatever the timing)
+  auto row_sum = [&](float s, float* buf) {
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (wpr == 1) return s;
+    if (lane == 0) buf[warp] = s;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + mr), "r"(tpr) : "memory");
+    s = lane < wpr ? buf[w0 + lane] : 0.f;
+#pragma unroll
+    for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return __shfl_sync(0xffffffffu, s, 0);
+  };
+  // r once more, for the paths that are hardly ever taken (with a residual as
+  // this thread has just stored it)
+  auto again = [&](int i, float2 (&v)[4]) {
+    unpack8(live && i < nv ? (RES ? op[i] : xp[i]) : make_uint4(0u, 0u, 0u, 0u), v);
+  };
+  float ss = row_sum(ss2.x + ss2.y, part[0]), up = 1.f;
+  // squares of bf16 values can pass fp32's range at both ends: such a row is
+  // summed again, scaled by a power of two
+  if (ss > 0x1p120f || (ss < 0x1p-80f && a.eps < 0x1p-60f)) {
+    up = ss > 0x1p120f ? 0x1p-64f : 0x1p64f;
+    float s2 = 0.f;
+    for (int j = 0; j < steps; ++j) {
+      float2 v[4];
+      again(j * tpr + tid, v);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        s2 = fmaf(up * v[k].x, up * v[k].x, s2);
+        s2 = fmaf(up * v[k].y, up * v[k].y, s2);
+      }
+    }
+    ss = row_sum(s2, part[1]);
+  }
+  const float inv = up * rsqrtf(fmaf(ss, inv_k, up * up * a.eps));
+  __syncwarp();
+  for (int l = lane; l < 2 * steps; l += 32) {
+    const int g = ((l >> 1) * tpr + (warp - w0) * 32 + 16 * (l & 1)) / 16;
+    if (live && g * 16 < nv) a.scales[(size_t)g * a.M + m] = scale_of(am_w[l] * inv);
+  }
+  if (__any_sync(0xffffffffu, odd || least * inv * (1.0f / 448.0f) < kFp8MinScale)) {
+    // the smallest scale, NaN, infinities, products r w out of fp32's range:
+    // the warp's blocks by the definition, v first
+    for (int j = 0; j < steps; ++j) {
       const int i = j * tpr + tid;
-      float v[8], w[8];
-      unpack8(r[j], v);
-      unpack8(kAhead ? wv[j] : weight(j), w);
+      float2 v[4], g[4];
+      again(i, v);
+      unpack8(i < nv ? __ldg(wp + i) : make_uint4(0u, 0u, 0u, 0u), g);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = v[k] * inv * w[k];
-      const float scale = block_scale(i < nv ? absmax8(v) : 0.f);
-      const uint2 c = codes8(v, __frcp_rn(scale));
-      if (m < a.M && i < nv) {
-        *reinterpret_cast<uint2*>(a.codes + (size_t)m * a.K + 8 * (size_t)i) = c;
+      for (int k = 0; k < 4; ++k) v[k] = make_float2(v[k].x * inv * g[k].x, v[k].y * inv * g[k].y);
+      const float scale = scale_of(block_max(absmax8(v)));
+      const uint2 c = codes8(v, rcp(scale));
+      if (live && i < nv) {
+        cp[i] = c;
         if ((lane & 15) == 0) a.scales[(size_t)(i / 16) * a.M + m] = scale;
       }
     }
@@ -210,10 +223,10 @@ __global__ void __launch_bounds__(256) fp8_quant_kernel(const Fp8ActArgs a, int 
   }
 #pragma unroll
   for (int u = 0; u < kPieces; ++u) {
-    float v[8];
+    float2 v[4];
     unpack8(x[u], v);
-    const float scale = block_scale(absmax8(v));
-    const uint2 c = codes8(v, __frcp_rn(scale));
+    const float scale = scale_of(block_max(absmax8(v)));
+    const uint2 c = codes8(v, rcp(scale));
     if (col[u] >= 0) {
       *reinterpret_cast<uint2*>(a.codes + (size_t)row[u] * a.K + col[u]) = c;
       if ((lane & 15) == 0) a.scales[(size_t)(col[u] / 128) * a.M + row[u]] = scale;
@@ -221,10 +234,11 @@ __global__ void __launch_bounds__(256) fp8_quant_kernel(const Fp8ActArgs a, int 
   }
 }
 
-cudaError_t launch_pdl(const void* fn, unsigned grid, int block, cudaStream_t s, void** args) {
+cudaError_t launch_pdl(const void* fn, unsigned grid, int block, int smem, cudaStream_t s, void** args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -233,17 +247,6 @@ cudaError_t launch_pdl(const void* fn, unsigned grid, int block, cudaStream_t s,
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
   return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-template <int VPT>
-cudaError_t launch_norm(const Fp8ActArgs& a, int tpr, int num_sms, cudaStream_t s) {
-  Fp8ActArgs args = a;
-  const int block = tpr < 256 ? 256 : tpr, rpc = block / tpr;
-  const long long ctas = ((long long)a.M + rpc - 1) / rpc, most = (long long)num_sms * (1024 / block);
-  void* ptrs[] = {&args, &tpr};
-  const void* fn = a.residual ? reinterpret_cast<const void*>(fp8_norm_kernel<VPT, true>)
-                              : reinterpret_cast<const void*>(fp8_norm_kernel<VPT, false>);
-  return launch_pdl(fn, (unsigned)(ctas < most ? ctas : most), block, s, ptrs);
 }
 
 }  // namespace
@@ -255,19 +258,27 @@ cudaError_t launch_fp8_act(const Fp8ActArgs& a, int num_sms, cudaStream_t s) {
     long long pieces = (long long)a.M * per_row;
     void* ptrs[] = {&args, &per_row, &pieces};
     return launch_pdl(reinterpret_cast<const void*>(fp8_quant_kernel), (unsigned)((pieces + 8 * kPieces - 1) / (8 * kPieces)),
-                      256, s, ptrs);
+                      256, 0, s, ptrs);
   }
-  // threads of a row: a power of two of warps, up to 8 vectors of 8 columns each
+  // warps of a row: one where there are rows enough to fill the SMs (no
+  // barrier, the least work beside the columns), more for fewer rows, but no
+  // more than the row has columns for
   const int nv = a.K / 8;
-  int vpt = a.M <= 2 * num_sms ? 1 : 2, tpr = 32;
-  while (tpr < 512 && tpr * vpt < nv) tpr *= 2;
-  while (tpr * vpt < nv) vpt *= 2;
-  switch (vpt) {
-    case 1: return launch_norm<1>(a, tpr, num_sms, s);
-    case 2: return launch_norm<2>(a, tpr, num_sms, s);
-    case 4: return launch_norm<4>(a, tpr, num_sms, s);
-    default: return launch_norm<8>(a, tpr, num_sms, s);
-  }
+  int wpr = 1;
+  while (wpr < 16 && (long long)a.M * wpr < 24ll * num_sms && wpr * 32 < nv) wpr *= 2;
+  const int warps = wpr < 8 ? 8 : wpr, rpc = warps / wpr;
+  Fp8ActArgs args = a;
+  float inv_k = (float)(1.0 / a.K);
+  void* ptrs[] = {&args, &wpr, &inv_k};
+  const int steps = (nv + 32 * wpr - 1) / (32 * wpr);
+  const void* fn[2][3] = {{reinterpret_cast<const void*>(fp8_norm_kernel<false, 1>),
+                           reinterpret_cast<const void*>(fp8_norm_kernel<false, 2>),
+                           reinterpret_cast<const void*>(fp8_norm_kernel<false, 4>)},
+                          {reinterpret_cast<const void*>(fp8_norm_kernel<true, 1>),
+                           reinterpret_cast<const void*>(fp8_norm_kernel<true, 2>),
+                           reinterpret_cast<const void*>(fp8_norm_kernel<true, 4>)}};
+  return launch_pdl(fn[a.residual ? 1 : 0][steps < 3 ? steps - 1 : 2], (unsigned)(((long long)a.M + rpc - 1) / rpc),
+                    32 * warps, warps * 2 * steps * 4, s, ptrs);
 }
 
 }  // namespace svdq
