@@ -522,10 +522,11 @@ svdq_status svdq_rope_tables(int M, int axes, int pairs, const long long* pos, c
   if (overlap(c, n) || rope_inputs_overlap(c, M, axes, pairs, pos, freq, axis) ||
       rope_inputs_overlap(n, M, axes, pairs, pos, freq, axis))
     return SVDQ_ERR_INVALID_ARG;
-  svdq_status st = device_info(nullptr, nullptr);
+  int sms = 0;
+  svdq_status st = device_info(nullptr, &sms);
   if (st != SVDQ_OK) return st;
   RopeArgs a{pos, freq, axis, nullptr, nullptr, 0, 0, M, axes, pairs, 0, 0, 0, factor};
-  return from_cuda(launch_rope_tables(a, cos_t, sin_t, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_rope_tables(a, cos_t, sin_t, sms, static_cast<cudaStream_t>(stream)));
 }
 
 svdq_status svdq_rope_apply(int M, int heads, int head_dim, int pairs, svdq_rope_layout layout, int axes,
@@ -543,11 +544,12 @@ svdq_status svdq_rope_apply(int M, int heads, int head_dim, int pairs, svdq_rope
   const Span sx = rows_span(x, M, width, ldx, 2), sy = rows_span(y, M, width, ldy, 2);
   if (overlap(sx, sy) && !(x == y && ldx == ldy)) return SVDQ_ERR_INVALID_ARG;
   if (rope_inputs_overlap(sy, M, axes, pairs, pos, freq, axis)) return SVDQ_ERR_INVALID_ARG;
-  svdq_status st = device_info(nullptr, nullptr);
+  int sms = 0;
+  svdq_status st = device_info(nullptr, &sms);
   if (st != SVDQ_OK) return st;
   RopeArgs a{pos, freq, axis, x, y, ldx, ldy, M, axes, pairs, heads, head_dim, layout == SVDQ_ROPE_HALF ? 1 : 0,
              factor};
-  return from_cuda(launch_rope_apply(a, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_rope_apply(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 svdq_status svdq_device_error(unsigned* bits) {

@@ -151,8 +151,8 @@ struct RopeArgs {
   int M, axes, pairs, heads, head_dim, half;
   float factor;
 };
-cudaError_t launch_rope_apply(const RopeArgs& a, cudaStream_t s);
-cudaError_t launch_rope_tables(const RopeArgs& a, float* cos_t, float* sin_t, cudaStream_t s);
+cudaError_t launch_rope_apply(const RopeArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_rope_tables(const RopeArgs& a, float* cos_t, float* sin_t, int num_sms, cudaStream_t s);
 
 cudaError_t launch_probe_convert(const float* in, long long n, uint8_t* e2m1, uint8_t* e4m3,
                                  uint16_t* bf16, cudaStream_t s);

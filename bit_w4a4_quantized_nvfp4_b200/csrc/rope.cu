@@ -6,7 +6,12 @@
 // turns are taken off by Cody and Waite's reduction: t - n * 2pi with 2pi in
 // two parts and fused multiply-adds, so that the remainder keeps its bits;
 // cos and sin of the remainder are fp32.
-#include "device.cuh"
+//
+// Bound by HBM: the heads are read and written once, 16 bytes a load. A CTA
+// has a few rows (or, while rows are few, a piece of one), loads its first
+// columns, then forms its rows' cos and sin once in shared memory for all
+// heads, so the angles' arithmetic runs under the loads.
+#include "fp8.cuh"
 #include "kernels.h"
 
 namespace svdq {
@@ -31,49 +36,220 @@ __device__ __forceinline__ long long rope_position(const RopeArgs& a, size_t m, 
   return a.pos[m * a.axes + (x >= 0 && x < a.axes ? x : 0)];
 }
 
-__global__ void __launch_bounds__(256) rope_tables_kernel(RopeArgs a, float* __restrict__ cos_t,
+__global__ void __launch_bounds__(256) rope_tables_kernel(const RopeArgs a, float* __restrict__ cos_t,
                                                           float* __restrict__ sin_t) {
-  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (size_t)a.M * a.pairs) return;
-  const size_t m = i / a.pairs;
-  const int p = (int)(i % a.pairs);
-  rope_turn(rope_position(a, m, p), a.freq[p], a.factor, cos_t[i], sin_t[i]);
+  if (threadIdx.x == 0) launch_dependents();
+  grid_dependency_wait();
+  // row and pair advance by a fixed stride: no division in the loop
+  const long long stride = (long long)gridDim.x * 256, first = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long dm = stride / a.pairs;
+  const int dp = (int)(stride - dm * a.pairs);
+  long long m = first / a.pairs;
+  int p = (int)(first - m * a.pairs);
+  while (m < a.M) {
+    float c, s;
+    rope_turn(rope_position(a, (size_t)m, p), a.freq[p], a.factor, c, s);
+    cos_t[m * a.pairs + p] = c;
+    sin_t[m * a.pairs + p] = s;
+    m += dm;
+    p += dp;
+    if (p >= a.pairs) {
+      p -= a.pairs;
+      ++m;
+    }
+  }
 }
 
-__global__ void __launch_bounds__(256) rope_apply_kernel(RopeArgs a) {
-  __shared__ float cs[kRopeMaxPairs], sn[kRopeMaxPairs];
-  const size_t m = blockIdx.x;
-  for (int i = threadIdx.x; i < a.pairs; i += 256)
-    rope_turn(rope_position(a, m, i), a.freq[i], a.factor, cs[i], sn[i]);
-  __syncthreads();
-  const uint16_t* x = a.x + m * (size_t)a.ldx;
-  uint16_t* y = a.y + m * (size_t)a.ldy;
-  for (int j = threadIdx.x; j < a.heads * a.pairs; j += 256) {
-    const int h = j / a.pairs, i = j % a.pairs;
-    const int p = h * a.head_dim + (a.half ? i : 2 * i), q = a.half ? p + a.pairs : p + 1;
-    const float u = bf16_bits_to_f32(x[p]), v = bf16_bits_to_f32(x[q]);
-    y[p] = (uint16_t)f32_to_bf16_bits(fmaf(u, cs[i], -v * sn[i]));
-    y[q] = (uint16_t)f32_to_bf16_bits(fmaf(u, sn[i], v * cs[i]));
+constexpr int kThreadsO = 256;
+constexpr int kUnits = 4;            // units a thread has in flight
+constexpr int kMaxAngles = 4096;     // cos and sin of a CTA's rows (32 KB)
+
+// How a row is cut: `upr` units, head by head `uph` of them, the first `rot`
+// of a head rotated (interleaved: 8 columns of 4 pairs; half: V columns and
+// their partners), the rest, where they are copied, rw columns each.
+struct RopePlan {
+  int rows, chunks;        // rows of a CTA; pieces of a row (one of the two is 1)
+  int upr, uph, rot, rw;
+  unsigned long long uph_magic, upr_magic;   // ceil(2^40 / d): u / d for u < 2^20
+};
+__device__ __forceinline__ int div_magic(int u, unsigned long long magic) {
+  return (int)(((unsigned long long)u * magic) >> 40);
+}
+
+template <int N>
+__device__ __forceinline__ void load_cols(const uint16_t* p, uint32_t (&r)[(N + 1) / 2]) {
+  if constexpr (N == 8) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
+  } else if constexpr (N == 4) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    r[0] = v.x; r[1] = v.y;
+  } else {
+    r[0] = *p;
   }
-  if (x == y) return;
-  const int rest = a.head_dim - 2 * a.pairs;
-  for (int j = threadIdx.x; j < a.heads * rest; j += 256) {
-    const int p = j / rest * a.head_dim + 2 * a.pairs + j % rest;
-    y[p] = x[p];
+}
+template <int N>
+__device__ __forceinline__ void store_cols(uint16_t* p, const uint32_t (&r)[(N + 1) / 2]) {
+  if constexpr (N == 8)
+    *reinterpret_cast<uint4*>(p) = make_uint4(r[0], r[1], r[2], r[3]);
+  else if constexpr (N == 4)
+    *reinterpret_cast<uint2*>(p) = make_uint2(r[0], r[1]);
+  else
+    *p = (uint16_t)r[0];
+}
+__device__ __forceinline__ float col(const uint32_t* r, int k) {
+  return __uint_as_float(k & 1 ? r[k >> 1] & 0xFFFF0000u : r[k >> 1] << 16);
+}
+
+// V: columns of a load. Interleaved V = 8 (pairs past the last are passed
+// through); half V = 8, 4 or 1 as the number of pairs divides.
+template <bool HALF, int V>
+__global__ void __launch_bounds__(kThreadsO) rope_apply_kernel(const RopeArgs a, const RopePlan pl) {
+  extern __shared__ float turn[];   // [rows][pairs] cos, then sin
+  const int P = a.pairs;
+  const long long m0 = (long long)(blockIdx.x / pl.chunks) * pl.rows;
+  const int rows = (int)min((long long)pl.rows, (long long)a.M - m0);
+  const int chunk = (int)(blockIdx.x % pl.chunks), per = (pl.upr + pl.chunks - 1) / pl.chunks;
+  const int u0 = chunk * per, u1 = pl.chunks > 1 ? min(pl.upr, u0 + per) : rows * pl.upr;
+  float* cs = turn;
+  float* sn = turn + pl.rows * P;
+  const bool inplace = a.x == a.y;
+  if (threadIdx.x == 0) launch_dependents();
+  // every input may be the previous kernel's output, y may still be read by it
+  grid_dependency_wait();
+
+  bool angles = false;
+  for (int ub = u0; ub < u1; ub += kThreadsO * kUnits) {
+    uint32_t lo[kUnits][(V + 1) / 2], hi[kUnits][(V + 1) / 2];
+    int row[kUnits], col0[kUnits], unit[kUnits];
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      const int u = ub + k * kThreadsO + (int)threadIdx.x;
+      unit[k] = -1;
+      if (u >= u1) continue;
+      row[k] = pl.chunks > 1 ? 0 : div_magic(u, pl.upr_magic);
+      const int ur = u - row[k] * pl.upr, h = div_magic(ur, pl.uph_magic);
+      unit[k] = ur - h * pl.uph;
+      col0[k] = h * a.head_dim;
+      const uint16_t* xp = a.x + (size_t)(m0 + row[k]) * (size_t)a.ldx + col0[k];
+      if (!HALF) {
+        load_cols<V>(xp + V * unit[k], lo[k]);
+      } else if (unit[k] < pl.rot) {
+        load_cols<V>(xp + V * unit[k], lo[k]);
+        load_cols<V>(xp + V * unit[k] + P, hi[k]);
+      }
+    }
+    if (!angles) {
+      for (int i = threadIdx.x; i < rows * P; i += kThreadsO) {
+        const int r = i / P, p = i - r * P;
+        rope_turn(rope_position(a, (size_t)(m0 + r), p), a.freq[p], a.factor, cs[i], sn[i]);
+      }
+      __syncthreads();
+      angles = true;
+    }
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      if (unit[k] < 0) continue;
+      const float* c = cs + row[k] * P;
+      const float* s = sn + row[k] * P;
+      uint16_t* yp = a.y + (size_t)(m0 + row[k]) * (size_t)a.ldy + col0[k];
+      if constexpr (!HALF) {
+        const int p0 = V / 2 * unit[k];
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+          if (p0 + i >= P) break;
+          const float u = col(lo[k], 2 * i), v = col(lo[k], 2 * i + 1), ct = c[p0 + i], st = s[p0 + i];
+          lo[k][i] = pack_bf16x2(fmaf(u, ct, -v * st), fmaf(u, st, v * ct));
+        }
+        store_cols<V>(yp + V * unit[k], lo[k]);
+      } else if (unit[k] < pl.rot) {
+        const int p0 = V * unit[k];
+        float o[V], w[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float u = col(lo[k], i), v = col(hi[k], i), ct = c[p0 + i], st = s[p0 + i];
+          o[i] = fmaf(u, ct, -v * st);
+          w[i] = fmaf(u, st, v * ct);
+        }
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+          lo[k][i / 2] = V == 1 ? f32_to_bf16_bits(o[i]) : pack_bf16x2(o[i], o[i + 1 < V ? i + 1 : i]);
+          hi[k][i / 2] = V == 1 ? f32_to_bf16_bits(w[i]) : pack_bf16x2(w[i], w[i + 1 < V ? i + 1 : i]);
+        }
+        store_cols<V>(yp + p0, lo[k]);
+        store_cols<V>(yp + p0 + P, hi[k]);
+      } else if (!inplace) {
+        const int at = 2 * P + pl.rw * (unit[k] - pl.rot);
+        const uint16_t* xp = a.x + (size_t)(m0 + row[k]) * (size_t)a.ldx + col0[k] + at;
+        if (pl.rw == 8)
+          *reinterpret_cast<uint4*>(yp + at) = *reinterpret_cast<const uint4*>(xp);
+        else
+          *reinterpret_cast<uint32_t*>(yp + at) = *reinterpret_cast<const uint32_t*>(xp);
+      }
+    }
   }
+}
+
+cudaError_t launch_rope(const void* fn, unsigned grid, int smem, cudaStream_t s, void** args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreadsO);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_rope_tables(const RopeArgs& a, float* cos_t, float* sin_t, cudaStream_t s) {
-  const size_t n = (size_t)a.M * a.pairs;
-  rope_tables_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a, cos_t, sin_t);
-  return cudaGetLastError();
+cudaError_t launch_rope_tables(const RopeArgs& a, float* cos_t, float* sin_t, int num_sms, cudaStream_t s) {
+  const long long blocks = ((long long)a.M * a.pairs + 255) / 256, most = 8ll * num_sms;
+  RopeArgs args = a;
+  void* ptrs[] = {&args, &cos_t, &sin_t};
+  return launch_rope(reinterpret_cast<const void*>(rope_tables_kernel), (unsigned)(blocks < most ? blocks : most), 0, s,
+                     ptrs);
 }
 
-cudaError_t launch_rope_apply(const RopeArgs& a, cudaStream_t s) {
-  rope_apply_kernel<<<(unsigned)a.M, 256, 0, s>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_rope_apply(const RopeArgs& a, int num_sms, cudaStream_t s) {
+  const bool inplace = a.x == a.y;
+  const int P = a.pairs, rest = a.head_dim - 2 * P;
+  const int v = !a.half ? 8 : P % 8 == 0 ? 8 : P % 4 == 0 ? 4 : 1;
+  RopePlan pl;
+  pl.rw = (2 * P) % 8 == 0 ? 8 : 2;
+  if (a.half) {
+    pl.rot = P / v;
+    pl.uph = pl.rot + (inplace ? 0 : rest / pl.rw);
+  } else {
+    pl.rot = (2 * P + 7) / 8;
+    pl.uph = inplace ? pl.rot : a.head_dim / 8;
+  }
+  pl.upr = pl.uph * a.heads;
+  // rows of a CTA: as many as give each thread its units, within the angles'
+  // room, and no more than leave every SM four CTAs; where that is one row and
+  // there are fewer rows than that, a row is cut into pieces of one unit a
+  // thread (each piece forms the row's angles again)
+  const long long spread = (long long)a.M / (4 * num_sms);
+  long long rows = kThreadsO * kUnits / pl.upr;
+  if (rows > kMaxAngles / P) rows = kMaxAngles / P;
+  if (rows > spread) rows = spread;
+  pl.rows = rows < 1 ? 1 : (int)rows;
+  pl.chunks = spread < 1 ? (pl.upr + kThreadsO - 1) / kThreadsO : 1;
+  if ((long long)a.M * pl.chunks > 8ll * num_sms) pl.chunks = 1;
+  pl.uph_magic = ((1ull << 40) + pl.uph - 1) / pl.uph;
+  pl.upr_magic = ((1ull << 40) + pl.upr - 1) / pl.upr;
+  const long long grid = ((long long)a.M + pl.rows - 1) / pl.rows * pl.chunks;
+  RopeArgs args = a;
+  void* ptrs[] = {&args, &pl};
+  const void* fn = !a.half  ? reinterpret_cast<const void*>(rope_apply_kernel<false, 8>)
+                   : v == 8 ? reinterpret_cast<const void*>(rope_apply_kernel<true, 8>)
+                   : v == 4 ? reinterpret_cast<const void*>(rope_apply_kernel<true, 4>)
+                            : reinterpret_cast<const void*>(rope_apply_kernel<true, 1>);
+  return launch_rope(fn, (unsigned)grid, pl.rows * P * 8, s, ptrs);
 }
 
 }  // namespace svdq

@@ -334,8 +334,8 @@ svdq_status svdq_rope_tables(int M, int axes, int pairs, const long long* pos, c
  * the columns past them unchanged. The Q and K sections of a grouped Q/K/V
  * row are adjacent, so one call with heads = query + key heads rotates both.
  * Out: y bf16 [M, heads * head_dim] (row stride ldy); y may be x itself (same
- *      address and stride: in place, only the rotated columns are touched);
- *      any other overlap gives SVDQ_ERR_INVALID_ARG.
+ *      address and stride: in place); any other overlap gives
+ *      SVDQ_ERR_INVALID_ARG.
  * Shapes: M >= 0 (M = 0 is a no-op), 1 <= pairs <= 512, 2 pairs <= head_dim,
  * head_dim % 8 == 0, heads * head_dim <= 2^20. x, y 16-byte aligned; the
  * others as svdq_rope_tables. */
