@@ -105,7 +105,7 @@ __device__ __forceinline__ float col(const uint32_t* r, int k) {
 // through); half V = 8, 4 or 1 as the number of pairs divides.
 template <bool HALF, int V>
 __global__ void __launch_bounds__(kThreadsO) rope_apply_kernel(const RopeArgs a, const RopePlan pl) {
-  extern __shared__ float turn[];   // [rows][pairs] cos, then sin
+  extern __shared__ __align__(16) float turn[];   // [rows][pairs] cos, then sin
   const int P = a.pairs;
   const long long m0 = (long long)(blockIdx.x / pl.chunks) * pl.rows;
   const int rows = (int)min((long long)pl.rows, (long long)a.M - m0);
@@ -155,19 +155,43 @@ __global__ void __launch_bounds__(kThreadsO) rope_apply_kernel(const RopeArgs a,
       uint16_t* yp = a.y + (size_t)(m0 + row[k]) * (size_t)a.ldy + col0[k];
       if constexpr (!HALF) {
         const int p0 = V / 2 * unit[k];
+        if (P % 4 == 0) {
+          if (p0 < P) {
+            const float4 ct = *reinterpret_cast<const float4*>(c + p0), st = *reinterpret_cast<const float4*>(s + p0);
+            const float cv[4] = {ct.x, ct.y, ct.z, ct.w}, sv[4] = {st.x, st.y, st.z, st.w};
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-          if (p0 + i >= P) break;
-          const float u = col(lo[k], 2 * i), v = col(lo[k], 2 * i + 1), ct = c[p0 + i], st = s[p0 + i];
-          lo[k][i] = pack_bf16x2(fmaf(u, ct, -v * st), fmaf(u, st, v * ct));
+            for (int i = 0; i < V / 2; ++i) {
+              const float u = col(lo[k], 2 * i), v = col(lo[k], 2 * i + 1);
+              lo[k][i] = pack_bf16x2(fmaf(u, cv[i], -v * sv[i]), fmaf(u, sv[i], v * cv[i]));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) {
+            if (p0 + i >= P) break;
+            const float u = col(lo[k], 2 * i), v = col(lo[k], 2 * i + 1), ct = c[p0 + i], st = s[p0 + i];
+            lo[k][i] = pack_bf16x2(fmaf(u, ct, -v * st), fmaf(u, st, v * ct));
+          }
         }
         store_cols<V>(yp + V * unit[k], lo[k]);
       } else if (unit[k] < pl.rot) {
         const int p0 = V * unit[k];
-        float o[V], w[V];
+        float o[V], w[V], cv[V], sv[V];
+        if constexpr (V >= 4) {
+#pragma unroll
+          for (int i = 0; i < V; i += 4) {
+            const float4 ct = *reinterpret_cast<const float4*>(c + p0 + i);
+            const float4 st = *reinterpret_cast<const float4*>(s + p0 + i);
+            cv[i] = ct.x; cv[i + 1] = ct.y; cv[i + 2] = ct.z; cv[i + 3] = ct.w;
+            sv[i] = st.x; sv[i + 1] = st.y; sv[i + 2] = st.z; sv[i + 3] = st.w;
+          }
+        } else {
+          cv[0] = c[p0];
+          sv[0] = s[p0];
+        }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float u = col(lo[k], i), v = col(hi[k], i), ct = c[p0 + i], st = s[p0 + i];
+          const float u = col(lo[k], i), v = col(hi[k], i), ct = cv[i], st = sv[i];
           o[i] = fmaf(u, ct, -v * st);
           w[i] = fmaf(u, st, v * ct);
         }
