@@ -171,9 +171,16 @@ def _at_least(t: torch.Tensor, dtype, nbytes: int, name: str) -> None:
         raise ValueError(f"{name}: {t.numel() * t.element_size()} bytes, need {nbytes}")
 
 
+# the current stream's handle without building a Stream object (3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _prec(p) -> int:
@@ -483,11 +490,20 @@ def _rows(t: torch.Tensor, name: str, cols: Optional[int] = None) -> int:
 
 def _addr(t: torch.Tensor, dev: int, name: str) -> int:
     """Device address of a CUDA tensor of any strides on device ``dev``."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
     if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError(f"{name}: expected a CUDA tensor")
         raise ValueError(f"{name}: tensor on {t.device}, but the current device is cuda:{dev}")
     return t.data_ptr()
+
+
+def _flat(t: Optional[torch.Tensor], dev: int, name: str):
+    """Device address of a contiguous CUDA tensor on device ``dev`` (None: none)."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return _addr(t, dev, name)
 
 
 def _current(t: torch.Tensor) -> int:
@@ -505,11 +521,12 @@ def _new(shape, dtype, device, stream) -> torch.Tensor:
 
 
 def _fp8_act_out(out: Optional[Fp8Act], M: int, K: int, device, stream) -> Fp8Act:
+    G = (K + 127) // 128
     if out is None:
-        return Fp8Act(M, K, _new((M, K), _F8, device, stream), _new((_blocks(K), M), torch.float32, device, stream))
+        return Fp8Act(M, K, _new((M, K), _F8, device, stream), _new((G, M), torch.float32, device, stream))
     _need(out.M == M and out.K == K, "out: Fp8Act of M {}, K {}", out.M, out.K)
     _is(out.codes, _F8, (M, K), "out.codes")
-    _is(out.scales, torch.float32, (_blocks(K), M), "out.scales")
+    _is(out.scales, torch.float32, (G, M), "out.scales")
     return out
 
 
@@ -520,7 +537,8 @@ def fp8_quantize_act(x: torch.Tensor, stream=None, out: Optional[Fp8Act] = None)
     dev = _current(x)
     out = _fp8_act_out(out, M, K, x.device, stream)
     _check("svdq_fp8_quantize_act", load().svdq_fp8_quantize_act(
-        M, K, _addr(x, dev, "x"), ldx, _ptr(out.codes, dev), _ptr(out.scales, dev), _stream(stream)))
+        M, K, _addr(x, dev, "x"), ldx, _flat(out.codes, dev, "out.codes"), _flat(out.scales, dev, "out.scales"),
+        _stream(stream)))
     return out
 
 
@@ -534,22 +552,25 @@ def fp8_norm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float, residua
     M, K = x.shape
     _is(weight, torch.bfloat16, (K,), "weight")
     dev = _current(x)
+    pr = po = None
     ldr = ldo = 0
     if residual is not None:
-        _need(residual.shape == x.shape, "residual: shape {}, x {}", tuple(residual.shape), tuple(x.shape))
+        _need(residual.shape == x.shape, "residual: shape {}, x {}", residual.shape, x.shape)
         ldr = _rows(residual, "residual")
+        pr = _addr(residual, dev, "residual")
         if residual_out is None:
             residual_out = _new((M, K), torch.bfloat16, x.device, stream)
-        _need(residual_out.shape == x.shape, "residual_out: shape {}, x {}", tuple(residual_out.shape),
-              tuple(x.shape))
-        ldo = _rows(residual_out, "residual_out")
+            ldo = (K + 7) // 8 * 8
+        else:
+            _need(residual_out.shape == x.shape, "residual_out: shape {}, x {}", residual_out.shape, x.shape)
+            ldo = _rows(residual_out, "residual_out")
+        po = _addr(residual_out, dev, "residual_out")
     else:
         _need(residual_out is None, "residual_out given without residual")
     out = _fp8_act_out(out, M, K, x.device, stream)
     _check("svdq_fp8_norm_quantize", load().svdq_fp8_norm_quantize(
-        M, K, _addr(x, dev, "x"), ldx, None if residual is None else _addr(residual, dev, "residual"), ldr,
-        _ptr(weight, dev), float(eps), None if residual is None else _addr(residual_out, dev, "residual_out"), ldo,
-        _ptr(out.codes, dev), _ptr(out.scales, dev), _stream(stream)))
+        M, K, _addr(x, dev, "x"), ldx, pr, ldr, _flat(weight, dev, "weight"), float(eps), po, ldo,
+        _flat(out.codes, dev, "out.codes"), _flat(out.scales, dev, "out.scales"), _stream(stream)))
     return out, residual_out
 
 
@@ -566,7 +587,8 @@ def fp8_pack_weight(W: torch.Tensor, stream=None, out: Optional[Fp8Weight] = Non
         _is(out.codes, _F8, (N, K), "out.codes")
         _is(out.scales, torch.float32, (_blocks(N), _blocks(K)), "out.scales")
     _check("svdq_fp8_pack_weight", load().svdq_fp8_pack_weight(
-        K, N, _ptr(W, dev), _ptr(out.codes, dev), _ptr(out.scales, dev), _stream(stream)))
+        K, N, _flat(W, dev, "W"), _flat(out.codes, dev, "out.codes"), _flat(out.scales, dev, "out.scales"),
+        _stream(stream)))
     return out
 
 
@@ -576,11 +598,11 @@ def fp8_linear(qa: Fp8Act, w: Fp8Weight, bias: Optional[torch.Tensor] = None, ou
     M, K, N = qa.M, qa.K, w.N
     _need(K == w.K, "activations have K = {}, the packed weight K = {}", K, w.K)
     _need(out_dtype == "bf16" or out_dtype == "f32", "out_dtype {!r}", out_dtype)
-    G = _blocks(K)
+    G = (K + 127) // 128
     _is(qa.codes, _F8, (M, K), "qa.codes")
     _is(qa.scales, torch.float32, (G, M), "qa.scales")
     _is(w.codes, _F8, (N, K), "w.codes")
-    _is(w.scales, torch.float32, (_blocks(N), G), "w.scales")
+    _is(w.scales, torch.float32, ((N + 127) // 128, G), "w.scales")
     if bias is not None:
         _is(bias, torch.bfloat16, (N,), "bias")
     want = torch.bfloat16 if out_dtype == "bf16" else torch.float32
@@ -590,8 +612,9 @@ def fp8_linear(qa: Fp8Act, w: Fp8Weight, bias: Optional[torch.Tensor] = None, ou
     else:
         _is(out, want, (M, N), "out")
     _check("svdq_fp8_linear", load().svdq_fp8_linear(
-        M, K, N, _ptr(qa.codes, dev), _ptr(qa.scales, dev), _ptr(w.codes, dev), _ptr(w.scales, dev),
-        _ptr(bias, dev), _ptr(out, dev), _OUT[out_dtype], _stream(stream)))
+        M, K, N, _flat(qa.codes, dev, "qa.codes"), _flat(qa.scales, dev, "qa.scales"), _flat(w.codes, dev, "w.codes"),
+        _flat(w.scales, dev, "w.scales"), _flat(bias, dev, "bias"), _flat(out, dev, "out"), _OUT[out_dtype],
+        _stream(stream)))
     return out
 
 
@@ -662,7 +685,8 @@ def _rope_inputs(positions: torch.Tensor, freqs: RopeFreqs, dev: int):
     pairs = f.shape[0]
     if freqs.axis is not None:
         _is(freqs.axis, torch.int32, (pairs,), "freqs.axis")
-    return M, axes, pairs, _ptr(positions, dev), _ptr(f, dev), _ptr(freqs.axis, dev)
+    return (M, axes, pairs, _flat(positions, dev, "positions"), _flat(f, dev, "freqs.freq"),
+            _flat(freqs.axis, dev, "freqs.axis"))
 
 
 def rope_tables(positions: torch.Tensor, freqs: RopeFreqs, stream=None):
@@ -673,7 +697,7 @@ def rope_tables(positions: torch.Tensor, freqs: RopeFreqs, stream=None):
     cos = _new((M, pairs), torch.float32, positions.device, stream)
     sin = _new((M, pairs), torch.float32, positions.device, stream)
     _check("svdq_rope_tables", load().svdq_rope_tables(M, axes, pairs, pp, pf, pa, float(freqs.factor),
-                                                       _ptr(cos, dev), _ptr(sin, dev), _stream(stream)))
+                                                       cos.data_ptr(), sin.data_ptr(), _stream(stream)))
     return cos, sin
 
 
