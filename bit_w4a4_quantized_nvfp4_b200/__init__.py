@@ -512,18 +512,19 @@ def _current(t: torch.Tensor) -> int:
     return torch.cuda.current_device()
 
 
-def _new(shape, dtype, device, stream) -> torch.Tensor:
-    """An output of a call on ``stream``: allocated for the stream that writes it."""
+def _new(rows: int, cols: int, dtype, device, stream) -> torch.Tensor:
+    """A contiguous output [rows, cols] of a call on ``stream``, allocated for
+    the stream that writes it (empty_strided takes two thirds of empty's time)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_strided((rows, cols), (max(cols, 1), 1), dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_strided((rows, cols), (max(cols, 1), 1), dtype=dtype, device=device)
 
 
 def _fp8_act_out(out: Optional[Fp8Act], M: int, K: int, device, stream) -> Fp8Act:
     G = (K + 127) // 128
     if out is None:
-        return Fp8Act(M, K, _new((M, K), _F8, device, stream), _new((G, M), torch.float32, device, stream))
+        return Fp8Act(M, K, _new(M, K, _F8, device, stream), _new(G, M, torch.float32, device, stream))
     _need(out.M == M and out.K == K, "out: Fp8Act of M {}, K {}", out.M, out.K)
     _is(out.codes, _F8, (M, K), "out.codes")
     _is(out.scales, torch.float32, (G, M), "out.scales")
@@ -559,7 +560,7 @@ def fp8_norm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float, residua
         ldr = _rows(residual, "residual")
         pr = _addr(residual, dev, "residual")
         if residual_out is None:
-            residual_out = _new((M, K), torch.bfloat16, x.device, stream)
+            residual_out = _new(M, K, torch.bfloat16, x.device, stream)
             ldo = (K + 7) // 8 * 8
         else:
             _need(residual_out.shape == x.shape, "residual_out: shape {}, x {}", residual_out.shape, x.shape)
@@ -580,8 +581,8 @@ def fp8_pack_weight(W: torch.Tensor, stream=None, out: Optional[Fp8Weight] = Non
     K, N = W.shape
     dev = _current(W)
     if out is None:
-        out = Fp8Weight(K, N, _new((N, K), _F8, W.device, stream),
-                        _new((_blocks(N), _blocks(K)), torch.float32, W.device, stream))
+        out = Fp8Weight(K, N, _new(N, K, _F8, W.device, stream),
+                        _new(_blocks(N), _blocks(K), torch.float32, W.device, stream))
     else:
         _need(out.K == K and out.N == N, "out: Fp8Weight of K {}, N {}", out.K, out.N)
         _is(out.codes, _F8, (N, K), "out.codes")
@@ -608,7 +609,7 @@ def fp8_linear(qa: Fp8Act, w: Fp8Weight, bias: Optional[torch.Tensor] = None, ou
     want = torch.bfloat16 if out_dtype == "bf16" else torch.float32
     dev = _current(qa.codes)
     if out is None:
-        out = _new((M, N), want, qa.codes.device, stream)
+        out = _new(M, N, want, qa.codes.device, stream)
     else:
         _is(out, want, (M, N), "out")
     _check("svdq_fp8_linear", load().svdq_fp8_linear(
@@ -694,8 +695,8 @@ def rope_tables(positions: torch.Tensor, freqs: RopeFreqs, stream=None):
     [M, axes], the tables that pack_rope (pairs = 64) and qkv_norm_rope take."""
     dev = _current(positions)
     M, axes, pairs, pp, pf, pa = _rope_inputs(positions, freqs, dev)
-    cos = _new((M, pairs), torch.float32, positions.device, stream)
-    sin = _new((M, pairs), torch.float32, positions.device, stream)
+    cos = _new(M, pairs, torch.float32, positions.device, stream)
+    sin = _new(M, pairs, torch.float32, positions.device, stream)
     _check("svdq_rope_tables", load().svdq_rope_tables(M, axes, pairs, pp, pf, pa, float(freqs.factor),
                                                        cos.data_ptr(), sin.data_ptr(), _stream(stream)))
     return cos, sin
