@@ -92,7 +92,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     }
     for (int b = 0; b < 4; ++b) {
       mbar_init(&sm.acc_full[b], 1);
-      mbar_init(&sm.acc_free[b], 2 * kDrainWarps);
+      mbar_init(&sm.acc_free[b], kDrainWarps);   // a half's four warps of both CTAs
     }
     mbar_init(&sm.mma_done, 2);
     fence_mbar_init();
@@ -152,17 +152,18 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       // step of 32 bytes 2 (addresses are in units of 16 bytes)
       const uint64_t a0 = make_sdesc(smem_u32(sm.stage[0]), 16, 1024, kLayoutSw128);
       const uint64_t b0 = make_sdesc(smem_u32(sm.stage[0]) + kABytes + h * (kBBytes / 2), 16, 1024, kLayoutSw128);
-      uint32_t it = 0, s = 0, sph = 0;   // K block, its stage and that stage's phase
+      uint32_t s = 0, sph = 0;   // stage and its phase
+      uint32_t aph = 3;          // phases of the half's two accumulators, a bit each
       bool ok = true;
       for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
-        for (int kb = 0; kb < p.G; ++kb, ++it) {
-          const uint32_t b = 2 * (it & 1) + h, aph = ((it >> 1) & 1) ^ 1;
+        for (int kb = 0; kb < p.G; ++kb) {
+          const uint32_t j = kb & 1, b = 2 * j + h;
           // both barriers tested at once: a test takes some 140 cycles
-          const bool rf = mbar_try_wait_relaxed(&sm.acc_free[b], aph);
+          const bool rf = mbar_try_wait_relaxed(&sm.acc_free[b], (aph >> j) & 1);
           const bool rs = mbar_try_wait(&sm.full[s], sph);
           if (!__all_sync(0xffffffffu, rs && rf) &&
               !(warp_wait(&sm.full[s], sph, p.wait_ns, p.err) &&
-                __all_sync(0xffffffffu, mbar_wait_relaxed(&sm.acc_free[b], aph, p.wait_ns, p.err)))) {
+                __all_sync(0xffffffffu, mbar_wait_relaxed(&sm.acc_free[b], (aph >> j) & 1, p.wait_ns, p.err)))) {
             ok = false;
             break;
           }
@@ -170,11 +171,12 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           const uint64_t da = a0 + (uint64_t)(s * (kStageBytes >> 4)), db = b0 + (uint64_t)(s * (kStageBytes >> 4));
           if (elect_one()) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mma_f8_pair(tmem + UN * b, da + 2 * j, db + 2 * j, kIdesc, j > 0 ? 1u : 0u);
+            for (int k = 0; k < 4; ++k) mma_f8_pair(tmem + UN * b, da + 2 * k, db + 2 * k, kIdesc, k > 0 ? 1u : 0u);
             tc_commit_pair(&sm.acc_full[b], 0x3);
             tc_commit_pair(&sm.empty[s], 0x3);
           }
           __syncwarp();
+          aph ^= 1u << j;
           if (++s == kStages) {
             s = 0;
             sph ^= 1;
@@ -189,88 +191,83 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
   } else {
     // ------------------------------------------------------------ drain
     regs_inc<kDrainRegs>();
-    const int q = warp & 3, e = warp - 4, w = e >> 2;
-    const uint32_t tq = tmem + 64 * w + ((uint32_t)(32 * q) << 16);
-    const uint32_t free0 = mapa_shared(smem_u32(&sm.acc_free[0]), 0);
-    uint32_t it = 0;
+    const int q = warp & 3, e = warp - 4, h = e >> 2;
+    const uint32_t tq = tmem + UN * h + ((uint32_t)(32 * q) << 16);   // accumulator 0 of the half; 1 is 2 UN on
+    const uint32_t freeb = mapa_shared(smem_u32(&sm.acc_free[h]), 0);
+    uint32_t ph[2] = {0, 0};                                          // the two accumulators' phases
     bool ok = true;
     for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
       int tm, tn;
       tile_at(tile, p, tm, tn);
       const int row0 = tm * 256 + (int)rank * BM + 32 * q;
-      const int n0 = tn * BN + 64 * w;
+      const int n0 = tn * BN + UN * h;
       // rows and columns past the end are not stored: any scale will do
       const float* sxp = p.x_scales + min(row0 + lane, p.M - 1);
-      const float* swp = p.w_scales + (size_t)(2 * tn) * p.G;
-      const size_t sw1 = 2 * tn + 1 <= (p.N - 1) / 128 ? p.G : 0;
-      float2 acc[64];   // columns n0 .. n0 + 63, then n0 + 128 .. n0 + 191
+      const float* swp = p.w_scales + (size_t)min(n0 / 128, (p.N - 1) / 128) * p.G;
+      float2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
-      // a K block's scales are loaded two blocks ahead of their use: beside
-      // the tiles' loads a read of L2 can take longer than one block
-      float sx[2], swa[2], swb[2];
+      // a K block's scale is loaded two blocks ahead of its use: beside the
+      // tiles' loads a read of L2 can take longer than one block
+      float sx[2], sw[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int kb = min(j, p.G - 1);
         sx[j] = __ldg(sxp + (size_t)kb * p.M);
-        swa[j] = __ldg(swp + kb);
-        swb[j] = __ldg(swp + sw1 + kb);
+        sw[j] = __ldg(swp + kb);
       }
-      // The units' sums are read as one stream of 16-column steps: the next
-      // step's load is in flight during this step's multiply-adds, across
-      // units too. The next unit's barrier is tested (not waited for) ahead,
-      // since a test takes some 150 cycles beside the MMAs' shared-memory reads.
-      if (!warp_wait(&sm.acc_full[2 * (it & 1)], (it >> 1) & 1, p.wait_ns, p.err)) break;
+      // The sums of consecutive K blocks are read as one stream of 16-column
+      // steps: the next step's load is in flight during this step's
+      // multiply-adds, across blocks too. The next block's barrier is tested
+      // (not waited for) ahead, since a test takes some 150 cycles beside the
+      // MMAs' shared-memory reads. Two blocks a turn, so that accumulators and
+      // barriers are fixed addresses: in the few instructions between two
+      // blocks every one counts.
+      if (!warp_wait(&sm.acc_full[h], ph[0], p.wait_ns, p.err)) break;
       tc_fence_after();
       uint32_t v[2][16];
-      tmem_ld16(tq + 2 * UN * (it & 1), v[0]);
+      tmem_ld16(tq, v[0]);
 #pragma unroll 1
       for (int kb0 = 0; kb0 < p.G && ok; kb0 += 2) {
 #pragma unroll
-        for (int jh = 0; jh < 4; ++jh) {
-          const int j = jh >> 1, h = jh & 1, kb = kb0 + j;
+        for (int j = 0; j < 2; ++j) {
+          const int kb = kb0 + j;
           if (kb >= p.G) break;
-          const uint32_t b = 2 * (it & 1) + h;
-          const uint32_t tb = tq + UN * b;
-          // the unit after this one: the other half, or the next K block's first
-          const uint32_t nb = h == 0 ? b + 1 : 2 * (~it & 1);
-          const uint32_t npar = ((h == 0 ? it : it + 1) >> 1) & 1;
-          const float s = sx[j] * (h ? swb[j] : swa[j]);
+          const float s = sx[j] * sw[j];
           const float2 s2 = make_float2(s, s);
+          ph[j] ^= 1;
           uint32_t ready = 0;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 8; ++c) {
             tmem_ld_wait();
             tmem_regs_ready(v[c & 1]);
-            if (c < 3) {
-              tmem_ld16(tb + 16 * (c + 1), v[(c + 1) & 1]);
+            if (c < 7) {
+              tmem_ld16(tq + 2 * UN * j + 16 * (c + 1), v[(c + 1) & 1]);
             } else {
               tc_fence_before();
-              mbar_arrive_if(lane == 0, free0 + 8 * b);
-              if (h == 0 || kb + 1 < p.G) {
-                if (!__all_sync(0xffffffffu, ready) && !warp_wait(&sm.acc_full[nb], npar, p.wait_ns, p.err)) {
+              mbar_arrive_if(lane == 0, freeb + 16 * j);
+              if (kb + 1 < p.G) {
+                if (!__all_sync(0xffffffffu, ready) &&
+                    !warp_wait(&sm.acc_full[2 * (j ^ 1) + h], ph[j ^ 1], p.wait_ns, p.err)) {
                   ok = false;
                   break;
                 }
                 tc_fence_after();
-                tmem_ld16(tq + UN * nb, v[0]);
+                tmem_ld16(tq + 2 * UN * (j ^ 1), v[0]);
               }
             }
-            if (c == 0) ready = mbar_try_wait_relaxed(&sm.acc_full[nb], npar);
-            if (h == 1 && c == 1) {
+            if (c == 1) {
               const int kn = min(kb + 2, p.G - 1);
               sx[j] = __ldg(sxp + (size_t)kn * p.M);
-              swa[j] = __ldg(swp + kn);
-              swb[j] = __ldg(swp + sw1 + kn);
+              sw[j] = __ldg(swp + kn);
             }
+            if (c == 4) ready = mbar_try_wait_relaxed(&sm.acc_full[2 * (j ^ 1) + h], ph[j ^ 1]);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              acc[32 * h + 8 * c + i] =
-                  __ffma2_rn(make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), s2,
-                             acc[32 * h + 8 * c + i]);
+              acc[8 * c + i] = __ffma2_rn(
+                  make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), s2, acc[8 * c + i]);
           }
           if (!ok) break;
-          if (h == 1) ++it;
         }
       }
       if (!ok) break;
@@ -278,7 +275,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       if (p.out_f32) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int n = n0 + 128 * (c >> 1) + 32 * (c & 1);
+          const int n = n0 + 32 * c;
           uint8_t* buf = sm.out[e][c % kSlots];
           if (lane == 0) bulk_wait_read<kSlots - 1>();
           __syncwarp();
@@ -305,7 +302,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       } else {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int n = n0 + 128 * c;
+          const int n = n0 + 64 * c;
           uint8_t* buf = sm.out[e][c % kSlots];
           if (lane == 0) bulk_wait_read<kSlots - 1>();
           __syncwarp();
