@@ -159,11 +159,11 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         for (int kb = 0; kb < p.G; ++kb) {
           const uint32_t j = kb & 1, b = 2 * j + h;
           // both barriers tested at once: a test takes some 140 cycles
-          const bool rf = mbar_try_wait_relaxed(&sm.acc_free[b], (aph >> j) & 1);
+          const bool rf = mbar_try_wait(&sm.acc_free[b], (aph >> j) & 1);
           const bool rs = mbar_try_wait(&sm.full[s], sph);
           if (!__all_sync(0xffffffffu, rs && rf) &&
               !(warp_wait(&sm.full[s], sph, p.wait_ns, p.err) &&
-                __all_sync(0xffffffffu, mbar_wait_relaxed(&sm.acc_free[b], (aph >> j) & 1, p.wait_ns, p.err)))) {
+                warp_wait(&sm.acc_free[b], (aph >> j) & 1, p.wait_ns, p.err))) {
             ok = false;
             break;
           }
@@ -261,7 +261,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
               sx[j] = __ldg(sxp + (size_t)kn * p.M);
               sw[j] = __ldg(swp + kn);
             }
-            if (c == 4) ready = mbar_try_wait_relaxed(&sm.acc_full[2 * (j ^ 1) + h], ph[j ^ 1]);
+            if (c == 4) ready = mbar_try_wait(&sm.acc_full[2 * (j ^ 1) + h], ph[j ^ 1]);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               acc[8 * c + i] = __ffma2_rn(
