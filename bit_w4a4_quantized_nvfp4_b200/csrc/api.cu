@@ -475,7 +475,7 @@ svdq_status svdq_fp8_norm_quantize(int M, int K, const uint16_t* x, long long ld
 
 svdq_status svdq_fp8_pack_weight(int K, int N, const float* W, uint8_t* codes, float* scales, void* stream) {
   if (K <= 0 || N <= 0) return SVDQ_ERR_INVALID_ARG;
-  if (K % 16 || N % 8) return SVDQ_ERR_SHAPE;
+  if (K % 16 || N % 8 || N > (1 << 23) - 128) return SVDQ_ERR_SHAPE;
   if (!W || !codes || !scales) return SVDQ_ERR_INVALID_ARG;
   if (!aligned16(W) || !aligned16(codes) || !aligned16(scales)) return SVDQ_ERR_ALIGN;
   svdq_status st = device_info(nullptr, nullptr);

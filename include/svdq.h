@@ -257,8 +257,7 @@ svdq_status awq_w4a16_linear(int M, int K, int N, const uint16_t* x, const uint8
  *                contiguous for the GEMM epilogue)
  *   weights:     codes u8 [N, K], scales fp32 [ceil(N/128), G]
  * A block's scale is max(max|v| / 448, 2^-126), its codes e4m3(v / scale). A
- * block that holds a NaN or an infinity stands for NaN throughout (its scale
- * is NaN or infinite, its codes NaN or 0).
+ * block that holds a NaN or an infinity stands for NaN throughout.
  * Row strides (ldx, ...) are in elements, multiples of 8, at least the row's
  * length; they may exceed it (a column range of a wider tensor). */
 
@@ -289,7 +288,7 @@ svdq_status svdq_fp8_norm_quantize(int M, int K, const uint16_t* x, long long ld
 
 /* svdq_fp8_pack_weight — offline pack of W fp32 [K, N] (y = x W).
  * Out: codes u8 [N, K], scales fp32 [ceil(N/128), G].
- * Shapes: K % 16 == 0, N % 8 == 0. Pointers 16-byte aligned. */
+ * Shapes: K % 16 == 0, N % 8 == 0, N <= 2^23 - 128. Pointers 16-byte aligned. */
 svdq_status svdq_fp8_pack_weight(int K, int N, const float* W, uint8_t* codes, float* scales, void* stream);
 
 /* svdq_fp8_linear — the 8-bit GEMM:

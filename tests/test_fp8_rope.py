@@ -72,6 +72,7 @@ def test_pack_and_linear_validation(lib):
     assert p(K=0) == S.INVALID_ARG
     assert p(K=24) == S.SHAPE
     assert p(N=12) == S.SHAPE
+    assert p(N=1 << 23) == S.SHAPE
     assert p(W=None) == S.INVALID_ARG
     assert p(codes=FAR + 8) == S.ALIGN
     c = _call(lib.svdq_fp8_linear, ["M", "K", "N", "xc", "xs", "wc", "ws", "b", "y", "out", "s"],

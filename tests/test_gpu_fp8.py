@@ -65,7 +65,8 @@ def test_quantize_act(M, K):
 
 @pytest.mark.parametrize("M,K,residual", [(1, 16, True), (1, 128, False), (1, 4096, True), (3, 144, True), (9, 1040, False),
                                           (129, 2064, True), (5, 12288, True), (4, 16400, True), (3, 32768, True),
-                                          (2, 32768, False), (700, 256, True), (33, 8192, False), (600, 5120, True)])
+                                          (2, 32768, False), (700, 256, True), (33, 8192, False), (600, 5120, True),
+                                          (3700, 1040, True), (3700, 2064, False), (4000, 128, True)])
 def test_norm_quantize(M, K, residual):
     x = _acts(M, K, M + K)
     w = (1 + 0.2 * torch.randn(K, generator=_gen(1), device="cuda")).to(torch.bfloat16)
@@ -80,10 +81,13 @@ def test_norm_quantize(M, K, residual):
     plain.check_codes(qa.codes, qa.scales, v, NORM_DELTA)
 
 
-def test_norm_quantize_extremes():
+@pytest.mark.parametrize("M", [9, 3700])
+def test_norm_quantize_extremes(M):
     """Rows of zeros (with eps and without values), tiny and huge rows, a NaN,
-    an infinity: each row as its definition gives, the rows beside it as ever."""
-    M, K = 9, 400
+    an infinity, products with the weight past fp32's range, blocks of zeros:
+    each row as its definition gives, the rows beside it as ever. Few rows are
+    spread over several warps, many have one each."""
+    K = 400
     x = _acts(M, K, 3)
     x[1] = 0.0
     x[2] *= 1e-30
@@ -91,16 +95,27 @@ def test_norm_quantize_extremes():
     x[4, 130] = float("nan")
     x[5, 7] = float("inf")
     x[6] = torch.finfo(torch.bfloat16).tiny
+    x[7, 128:256] = 0.0
     w = torch.ones(K, device="cuda", dtype=torch.bfloat16)
     qa, _ = svdq.fp8_norm_quantize(x, w, 1e-6)
     _ok()
-    fine = [0, 1, 2, 3, 6, 7, 8]
+    fine = [m for m in range(M) if m not in (4, 5)]
     v, _ = plain.norm64(x, w, 1e-6)
     plain.check_codes(qa.codes[fine], qa.scales[:, fine], v[fine], NORM_DELTA)
     got = qa.codes.float() * plain.spread(qa.scales, K)
     assert got[4].isnan().all()          # the NaN is in the row's mean square
     assert got[5, 7].isnan()             # inf / inf; the other values of the row go to 0
     assert (qa.codes[1].float() == 0).all() and (qa.scales[:, 1] == plain.MIN_SCALE).all()
+    assert (qa.codes[7, 128:256].float() == 0).all()
+    x[8] = 1e30
+    w[:] = 1e20
+    w[5] = 1e-30
+    qa, _ = svdq.fp8_norm_quantize(x, w, 0.0, residual=torch.zeros_like(x))
+    _ok()
+    v, _ = plain.norm64(x, w, 0.0)
+    fine = [m for m in range(M) if m not in (1, 4, 5)]
+    plain.check_codes(qa.codes[fine], qa.scales[:, fine], v[fine], NORM_DELTA)
+    assert (qa.codes[1].float() * plain.spread(qa.scales, K)[1]).isnan().all()   # 0 / 0
 
 
 def test_quantize_extremes():
