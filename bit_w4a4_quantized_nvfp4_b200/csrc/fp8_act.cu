@@ -213,16 +213,22 @@ __global__ void __launch_bounds__(256) fp8_quant_kernel(const Fp8ActArgs a, int 
   if (threadIdx.x == 0) launch_dependents();
   grid_dependency_wait();
   const long long p0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kPieces;
+  // one division a thread (in 32 bits where the count allows), then steps
+  long long r0 = pieces >> 31 ? p0 / per_row : (long long)((uint32_t)p0 / (uint32_t)per_row);
+  int c0 = (int)(p0 - r0 * per_row);
   uint4 x[kPieces];
   long long row[kPieces];
   int col[kPieces];
 #pragma unroll
   for (int u = 0; u < kPieces; ++u) {
-    const long long p = p0 + u;
-    row[u] = p / per_row;
-    col[u] = (int)(p - row[u] * per_row) * 256 + 8 * lane;
-    const bool in = p < pieces && col[u] < a.K;
+    row[u] = r0;
+    col[u] = c0 * 256 + 8 * lane;
+    const bool in = p0 + u < pieces && col[u] < a.K;
     if (!in) col[u] = -1;
+    if (++c0 == per_row) {
+      c0 = 0;
+      ++r0;
+    }
     x[u] = in ? *reinterpret_cast<const uint4*>(a.x + (size_t)row[u] * (size_t)a.ldx + col[u])
               : make_uint4(0u, 0u, 0u, 0u);
   }

@@ -3,7 +3,7 @@
 //
 // A block's product is one accumulator of the tensor cores; the scales are
 // fp32 and differ from block to block of 128 along K, so a block's sums leave
-// tensor memory before the next block may use their place, and are added,
+// tensor memory before a later block may use their place, and are added,
 // scaled, to sums in registers. That drain (one fused multiply-add for every
 // 128 products) is the second bound beside the MMA rate: 32,768 sums per SM
 // and K block of 512 MMA cycles.
@@ -11,17 +11,38 @@
 // Persistent, warp-specialised CTA pairs (cluster of 2, cta_group::2), each
 // with a 256 x 256 tile of y:
 //   warp 0       TMA producer (both CTAs): per K block this CTA's 128 rows of A
-//                and 128 rows of B, 128-byte rows, 128B-swizzled
-//   warp 1       MMA issuer (leader CTA): per K block two products of N = 128
-//                (column halves), each into one of its half's two accumulators
+//                and 2 x 64 rows of B, 128-byte rows, 128B-swizzled
+//   warps 1, 3   MMA issuers (leader CTA), one for each 128-column half of the
+//                tile: per K block a product of 256 x 128 x 128 into one of the
+//                half's two accumulators
 //   warp 2       tensor-memory allocation
 //   warps 4..11  drain (both CTAs), two warps per lane quadrant, one for each
-//                column half: a thread is a row, its 128 sums stay in
-//                registers over the whole K loop. A half is one 128-wide
-//                weight block, so a K block has one combined scale per thread.
-//                At the end bias, rounding, TMA store through 4 KB of staging.
-// Four accumulators of 128 columns (rather than two of 256): while one is
-// drained and handed back the other three take 768 cycles of MMAs.
+//                column half: a thread is a row, its 128 sums stay in registers
+//                over the whole K loop. A half is one 128-wide weight block, so
+//                a K block has one combined scale per thread. At the end bias,
+//                rounding, TMA store through staging.
+// Why this shape:
+//   - 256 x 256 per pair is what tensor memory holds twice (4 x 128 columns) and
+//     keeps the operands at 64 bytes per SM and cycle; L2 was seen to deliver
+//     some 50, so a smaller tile would wait for its operands.
+//   - Hand-overs cost more than the columns do. A barrier test takes some 140
+//     cycles beside the MMAs' shared-memory reads, an accumulator's way from
+//     the issuer through the drain and back several hundred. So a drain warp
+//     has one hand-over per K block (128 columns; units of 64 columns, two
+//     hand-overs, took 496 us at 8192^3, this 463), the next block's barrier is
+//     tested ahead, the issuers test both their barriers at once, and each half
+//     has its own issuer and its own two accumulators, so that one half's
+//     hand-over runs under the other's MMAs (one issuer with N = 256 products
+//     and two accumulators for both halves: 478 against 469).
+//   - Output straight from the registers, 32 bytes a store, was slower than
+//     the staging (522 us against 510 at 8192^3, 79 against 69 at 4608 x 1024 x
+//     9216): a thread's stores are rows apart.
+// Measured: 8192^3 463 us (2.37 PFLOP/s; the measured bf16 rate is 1.65 in
+// bursts, so 0.72 of twice that), 4608 x 4096 x 12288 208 us (2.23). Both run
+// into the 1000 W limit: at 463 us the SMs have gone down to 1.36 GHz, a copy
+// without the drain's arithmetic and loads takes 425 us at the same power, and
+// back to back for a second the same product takes 553 us (1.99 PFLOP/s, 1.44
+// times the bf16 rate under the same limit). What bounds it now is energy.
 #include "fp8.cuh"
 #include "kernels.h"
 
