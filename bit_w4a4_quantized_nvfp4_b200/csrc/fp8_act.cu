@@ -6,8 +6,8 @@
 // Bound by HBM: 3 bytes an element, 7 with a residual. Measured from HBM
 // (launches in a row): norm + residual 4608 x 4096 24.1 us, 5.5 TB/s, 0.85 of
 // the measured copy rate (20.4 us at that rate); 8192 x 8192 77.9 us, 0.93;
-// norm alone 4608 x 12288 33.0 us, 0.79; without the norm 4608 x 12288 33.4 us,
-// 0.79. What is left is the columns' arithmetic (some ten instructions each)
+// norm alone 4608 x 12288 33.0 us, 0.79; without the norm 4608 x 12288 27.6 us,
+// 0.95. What is left of the norm's is the columns' arithmetic (some ten instructions each)
 // and, at 4608 rows, one wave's start and end.
 //
 // A lane holds 8 consecutive columns (16 bytes of bf16), so 16 lanes are one
@@ -17,8 +17,7 @@
 // value the next layer reads.
 //
 // Norm: one pass, a row to a warp (to several while rows are few). Without the
-// norm blocks are independent: a warp takes four pieces of 256 columns at a
-// time.
+// norm blocks are independent: a warp takes two pieces of 256 columns at a time.
 #include "fp8.cuh"
 #include "kernels.h"
 
@@ -206,7 +205,10 @@ __global__ void __launch_bounds__(512, 2) fp8_norm_kernel(const Fp8ActArgs a, in
 }
 
 // -------------------------------------------------------------- no norm
-constexpr int kPieces = 4;   // pieces of 256 columns a warp loads at once
+// Pieces of 256 columns a warp loads at once: two leave 30 registers, so the SM
+// is full of warps (4608 x 12288: 28.2 us; four 32.6, one 35.1). The row is read
+// once and marked so (27.6).
+constexpr int kPieces = 2;
 
 __global__ void __launch_bounds__(256) fp8_quant_kernel(const Fp8ActArgs a, int per_row, long long pieces) {
   const int lane = threadIdx.x & 31;
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(256) fp8_quant_kernel(const Fp8ActArgs a, int 
       c0 = 0;
       ++r0;
     }
-    x[u] = in ? *reinterpret_cast<const uint4*>(a.x + (size_t)row[u] * (size_t)a.ldx + col[u])
+    x[u] = in ? __ldcs(reinterpret_cast<const uint4*>(a.x + (size_t)row[u] * (size_t)a.ldx + col[u]))
               : make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
