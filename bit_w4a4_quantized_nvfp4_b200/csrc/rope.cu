@@ -10,7 +10,10 @@
 // Bound by HBM: the heads are read and written once, 16 bytes a load. A CTA
 // has a few rows (or, while rows are few, a piece of one), loads its first
 // columns, then forms its rows' cos and sin once in shared memory for all
-// heads, so the angles' arithmetic runs under the loads.
+// heads, so the angles' arithmetic runs under the loads. Measured: 16384 rows of
+// 64 heads of 128, half layout, whole heads, 82.0 us (6.55 TB/s, the measured
+// copy rate); interleaved with half of each head rotated 87.1 us (0.95).
+// Tables are bound by the functions' arithmetic: 65536 x 64 in 14.4 us.
 #include "fp8.cuh"
 #include "kernels.h"
 
@@ -61,7 +64,9 @@ __global__ void __launch_bounds__(256) rope_tables_kernel(const RopeArgs a, floa
 }
 
 constexpr int kThreadsO = 256;
-constexpr int kUnits = 4;            // units a thread has in flight
+// Units a thread has in flight: two (interleaved 87.1 us at 16384 x 64 x 128,
+// in 40 registers; four 90.0 in 63, one 90.1).
+constexpr int kUnits = 2;
 constexpr int kMaxAngles = 4096;     // cos and sin of a CTA's rows (32 KB)
 
 // How a row is cut: `upr` units, head by head `uph` of them, the first `rot`
