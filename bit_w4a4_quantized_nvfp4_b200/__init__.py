@@ -175,11 +175,13 @@ def _at_least(t: torch.Tensor, dtype, nbytes: int, name: str) -> None:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream=None):
+def _stream(stream=None, dev: Optional[int] = None):
+    """Handle of ``stream``, or of the current one on the current device
+    (``dev``, when the caller has already read it)."""
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device() if dev is None else dev)
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -539,7 +541,7 @@ def fp8_quantize_act(x: torch.Tensor, stream=None, out: Optional[Fp8Act] = None)
     out = _fp8_act_out(out, M, K, x.device, stream)
     _check("svdq_fp8_quantize_act", load().svdq_fp8_quantize_act(
         M, K, _addr(x, dev, "x"), ldx, _flat(out.codes, dev, "out.codes"), _flat(out.scales, dev, "out.scales"),
-        _stream(stream)))
+        _stream(stream, dev)))
     return out
 
 
@@ -571,7 +573,7 @@ def fp8_norm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float, residua
     out = _fp8_act_out(out, M, K, x.device, stream)
     _check("svdq_fp8_norm_quantize", load().svdq_fp8_norm_quantize(
         M, K, _addr(x, dev, "x"), ldx, pr, ldr, _flat(weight, dev, "weight"), float(eps), po, ldo,
-        _flat(out.codes, dev, "out.codes"), _flat(out.scales, dev, "out.scales"), _stream(stream)))
+        _flat(out.codes, dev, "out.codes"), _flat(out.scales, dev, "out.scales"), _stream(stream, dev)))
     return out, residual_out
 
 
@@ -589,7 +591,7 @@ def fp8_pack_weight(W: torch.Tensor, stream=None, out: Optional[Fp8Weight] = Non
         _is(out.scales, torch.float32, (_blocks(N), _blocks(K)), "out.scales")
     _check("svdq_fp8_pack_weight", load().svdq_fp8_pack_weight(
         K, N, _flat(W, dev, "W"), _flat(out.codes, dev, "out.codes"), _flat(out.scales, dev, "out.scales"),
-        _stream(stream)))
+        _stream(stream, dev)))
     return out
 
 
@@ -615,7 +617,7 @@ def fp8_linear(qa: Fp8Act, w: Fp8Weight, bias: Optional[torch.Tensor] = None, ou
     _check("svdq_fp8_linear", load().svdq_fp8_linear(
         M, K, N, _flat(qa.codes, dev, "qa.codes"), _flat(qa.scales, dev, "qa.scales"), _flat(w.codes, dev, "w.codes"),
         _flat(w.scales, dev, "w.scales"), _flat(bias, dev, "bias"), _flat(out, dev, "out"), _OUT[out_dtype],
-        _stream(stream)))
+        _stream(stream, dev)))
     return out
 
 
@@ -698,7 +700,7 @@ def rope_tables(positions: torch.Tensor, freqs: RopeFreqs, stream=None):
     cos = _new(M, pairs, torch.float32, positions.device, stream)
     sin = _new(M, pairs, torch.float32, positions.device, stream)
     _check("svdq_rope_tables", load().svdq_rope_tables(M, axes, pairs, pp, pf, pa, float(freqs.factor),
-                                                       cos.data_ptr(), sin.data_ptr(), _stream(stream)))
+                                                       cos.data_ptr(), sin.data_ptr(), _stream(stream, dev)))
     return cos, sin
 
 
@@ -724,7 +726,7 @@ def rope_apply(x: torch.Tensor, heads: int, head_dim: int, positions: torch.Tens
         _need(out.shape[0] == M, "out: {} rows, x has {}", out.shape[0], M)
     _check("svdq_rope_apply", load().svdq_rope_apply(
         M, heads, head_dim, pairs, _ROPE_LAYOUT[layout], axes, pp, pf, pa, float(freqs.factor), _addr(x, dev, "x"),
-        ldx, _addr(out, dev, "out"), ldy, _stream(stream)))
+        ldx, _addr(out, dev, "out"), ldy, _stream(stream, dev)))
     return out
 
 
