@@ -56,7 +56,7 @@ constexpr int kBBytes = (BN / 2) * BK;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kDrainWarps = 8;
 constexpr int kThreads = 128 + 32 * kDrainWarps;
-constexpr int kSlots = 2, kSlotBytes = 32 * 128;   // output staging per drain warp
+constexpr int kSlots = 2, kSlotBytes = 32 * 128;   // output staging per drain warp (the bf16 columns)
 constexpr uint32_t kTmemCols = 512;
 constexpr int UN = 128;                        // columns of a unit: one accumulator
 constexpr uint32_t kIdesc = f8_idesc(2 * BM, UN);
@@ -83,6 +83,12 @@ struct Params {
   unsigned* err;
   unsigned long long wait_ns;
 };
+
+// bias of 8 columns from n on (n % 8 == 0, n + 8 <= N)
+__device__ __forceinline__ uint4 bias8(const Params& p, int n) {
+  const uint32_t* b = reinterpret_cast<const uint32_t*>(p.bias + n);
+  return make_uint4(__ldg(b), __ldg(b + 1), __ldg(b + 2), __ldg(b + 3));
+}
 
 // Tiles in groups of kGroupM tile rows, down the rows first: the tiles in
 // work at one time span about as many rows as columns, so that both operands
@@ -300,17 +306,17 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           uint8_t* buf = sm.out[e][c % kSlots];
           if (lane == 0) bulk_wait_read<kSlots - 1>();
           __syncwarp();
+          uint4 b8;
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
             float2 lo = acc[16 * c + 2 * u], hi = acc[16 * c + 2 * u + 1];
-            if (p.bias && n + 4 * u < p.N) {
-              const uint32_t b0 = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n + 4 * u));
-              const uint32_t b1 = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n + 4 * u + 2));
-              lo.x += bf16_bits_to_f32(b0 & 0xFFFFu);
-              lo.y += bf16_bits_to_f32(b0 >> 16);
-              hi.x += bf16_bits_to_f32(b1 & 0xFFFFu);
-              hi.y += bf16_bits_to_f32(b1 >> 16);
-            }
+            // the bias of 8 columns serves two of the 16-byte pieces
+            if (u % 2 == 0) b8 = p.bias && n + 4 * u < p.N ? bias8(p, n + 4 * u) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t b0 = u % 2 ? b8.z : b8.x, b1 = u % 2 ? b8.w : b8.y;
+            lo.x += bf16_bits_to_f32(b0 & 0xFFFFu);
+            lo.y += bf16_bits_to_f32(b0 >> 16);
+            hi.x += bf16_bits_to_f32(b1 & 0xFFFFu);
+            hi.y += bf16_bits_to_f32(b1 >> 16);
             *reinterpret_cast<float4*>(buf + lane * 128 + ((u ^ (lane & 7)) * 16)) = make_float4(lo.x, lo.y, hi.x, hi.y);
           }
           fence_proxy_async_smem();
@@ -321,33 +327,33 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           }
         }
       } else {
+        // both pieces, then one fence for the two copies
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < kSlots; ++c) {
           const int n = n0 + 64 * c;
-          uint8_t* buf = sm.out[e][c % kSlots];
-          if (lane == 0) bulk_wait_read<kSlots - 1>();
-          __syncwarp();
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
+            uint4 b8 = make_uint4(0u, 0u, 0u, 0u);
+            if (p.bias && n + 8 * u < p.N) b8 = bias8(p, n + 8 * u);
+            const uint32_t bw[4] = {b8.x, b8.y, b8.z, b8.w};
             uint32_t w4[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              float2 a = acc[32 * c + 4 * u + k];
-              if (p.bias && n + 8 * u < p.N) {
-                const uint32_t bw = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n + 8 * u + 2 * k));
-                a.x += bf16_bits_to_f32(bw & 0xFFFFu);
-                a.y += bf16_bits_to_f32(bw >> 16);
-              }
-              w4[k] = pack_bf16x2(a.x, a.y);
+              const float2 a = acc[32 * c + 4 * u + k];
+              w4[k] = pack_bf16x2(a.x + bf16_bits_to_f32(bw[k] & 0xFFFFu), a.y + bf16_bits_to_f32(bw[k] >> 16));
             }
-            *reinterpret_cast<uint4*>(buf + lane * 128 + ((u ^ (lane & 7)) * 16)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+            *reinterpret_cast<uint4*>(sm.out[e][c] + lane * 128 + ((u ^ (lane & 7)) * 16)) =
+                make_uint4(w4[0], w4[1], w4[2], w4[3]);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (row0 < p.M && n < p.N) tma_store_2d(&tm_y, buf, n, row0);
-            bulk_commit();
-          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (row0 < p.M && n0 < p.N) tma_store_2d(&tm_y, sm.out[e][0], n0, row0);
+          if (row0 < p.M && n0 + 64 < p.N) tma_store_2d(&tm_y, sm.out[e][1], n0 + 64, row0);
+          bulk_commit();
         }
       }
     }

@@ -279,6 +279,47 @@ def test_linear_each_block_has_its_scale(M):
         assert ((f.double() - y64).abs() <= plain.linear_bound(mag, K)).all()
 
 
+@pytest.mark.parametrize("M", [5, 40, 600])
+def test_linear_bias_at_any_four_bytes(M):
+    """A bias that starts 4, 8 and 12 bytes past a 16-byte boundary, both outputs."""
+    K, N = 272, 392
+    qa = svdq.Fp8Act(M, K, _codes(M, K, 1), _positive(3, M, seed=2))
+    w = svdq.Fp8Weight(K, N, _codes(N, K, 3), _positive(4, 3, seed=4))
+    many = torch.randn(N + 8, generator=_gen(5), device="cuda").to(torch.bfloat16)
+    for at in (0, 2, 4, 6):
+        b = many[at:at + N]
+        y64, mag = plain.linear64(qa.codes, qa.scales, w.codes, w.scales, b)
+        f, h = svdq.fp8_linear(qa, w, b, out_dtype="f32"), svdq.fp8_linear(qa, w, b)
+        _ok()
+        assert ((f.double() - y64).abs() <= plain.linear_bound(mag, K)).all()
+        assert torch.equal(f.to(torch.bfloat16), h)
+
+
+def test_two_streams_at_once():
+    """Calls of every kernel on two streams, in each other's way: the bits of
+    the same calls one after another."""
+    K, N = 2064, 1032
+    w = svdq.Fp8Weight(K, N, _codes(N, K, 3), _positive(9, 17, seed=4))
+    acts = [svdq.Fp8Act(M, K, _codes(M, K, M), _positive(17, M, seed=M + 1)) for M in (1, 20, 70, 300, 3000)]
+    x, g = _acts(500, K, 9), torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    want = [svdq.fp8_linear(a, w) for a in acts]
+    qa, _ = svdq.fp8_norm_quantize(x, g, 1e-6)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for rep in range(20):
+        for i, s in enumerate(streams):
+            for a in acts[::1 if i else -1]:
+                got[i].append(svdq.fp8_linear(a, w, stream=s))
+            got[i].append(svdq.fp8_norm_quantize(x, g, 1e-6, stream=s)[0].codes)
+    _ok()
+    for i in range(2):
+        for k, y in enumerate(got[i]):
+            k %= 6
+            ref = qa.codes if k == 5 else want[k if i else 4 - k]
+            assert torch.equal(y.view(torch.uint8), ref.view(torch.uint8))
+
+
 @pytest.mark.parametrize("M", [1, 20, 64, 130])
 def test_linear_nan_stays_in_its_row(M):
     K, N = 400, 264
