@@ -15,7 +15,7 @@
 //   warps 1, 3   MMA issuers (leader CTA), one for each 128-column half of the
 //                tile: per K block a product of 256 x 128 x 128 into one of the
 //                half's two accumulators
-//   warp 2       tensor-memory allocation
+//   warp 2       tensor-memory allocation, then the output copies (bf16)
 //   warps 4..11  drain (both CTAs), two warps per lane quadrant, one for each
 //                column half: a thread is a row, its 128 sums stay in registers
 //                over the whole K loop. A half is one 128-wide weight block, so
@@ -70,6 +70,7 @@ struct Smem {
   uint8_t out[kDrainWarps][kSlots][kSlotBytes];
   uint64_t full[kStages], empty[kStages];
   uint64_t acc_full[4], acc_free[4], mma_done;
+  uint64_t out_ready[kDrainWarps], out_free;
   uint32_t tmem_base;
 };
 
@@ -122,6 +123,8 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       mbar_init(&sm.acc_free[b], kDrainWarps);   // a half's four warps of both CTAs
     }
     mbar_init(&sm.mma_done, 2);
+    for (int e = 0; e < kDrainWarps; ++e) mbar_init(&sm.out_ready[e], 1);
+    mbar_init(&sm.out_free, 1);
     fence_mbar_init();
     tma_prefetch_desc(&tm_a);
     tma_prefetch_desc(&tm_b);
@@ -214,6 +217,31 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       if (elect_one()) tc_commit_pair(&sm.mma_done, 0x1);
       __syncwarp();
       (void)warp_wait(&sm.mma_done, 0, p.wait_ns, p.err);
+    } else if (warp == 2 && !p.out_f32) {
+      // ---------------------------------------------------------- output copies
+      uint32_t tl = 0;
+      bool ok = true;
+      for (int tile = pair; tile < num_tiles && ok; tile += npairs, ++tl) {
+        int tm, tn;
+        tile_at(tile, p, tm, tn);
+        for (int e = 0; e < kDrainWarps; ++e) {
+          if (!warp_wait(&sm.out_ready[e], tl & 1, p.wait_ns, p.err)) { ok = false; break; }
+          const int m = tm * 256 + (int)rank * BM + 32 * (e & 3), n = tn * BN + UN * (e >> 2);
+          if (lane == 0) {
+            if (m < p.M && n < p.N) tma_store_2d(&tm_y, sm.out[e][0], n, m);
+            if (m < p.M && n + 64 < p.N) tma_store_2d(&tm_y, sm.out[e][1], n + 64, m);
+            bulk_commit();
+          }
+          __syncwarp();
+        }
+        if (lane == 0) {
+          bulk_wait_read<0>();
+          mbar_arrive(&sm.out_free);
+        }
+        __syncwarp();
+      }
+      if (lane == 0) bulk_wait<0>();
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ drain
@@ -222,27 +250,35 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     const uint32_t tq = tmem + UN * h + ((uint32_t)(32 * q) << 16);   // accumulator 0 of the half; 1 is 2 UN on
     const uint32_t freeb = mapa_shared(smem_u32(&sm.acc_free[h]), 0);
     uint32_t ph[2] = {0, 0};                                          // the two accumulators' phases
-    bool ok = true;
-    for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
+    // A tile's row and columns for this warp, and its first two K blocks'
+    // scales, loaded ahead of the previous tile's output. (Rows and columns past
+    // the end are not stored: any scale will do.) Later blocks' scales are
+    // loaded two blocks ahead of their use: beside the tiles' loads a read of L2
+    // can take longer than one block.
+    int row0 = 0, n0 = 0;
+    const float *sxp = nullptr, *swp = nullptr;
+    float sx[2], sw[2];
+    auto open = [&](int tile) {
       int tm, tn;
       tile_at(tile, p, tm, tn);
-      const int row0 = tm * 256 + (int)rank * BM + 32 * q;
-      const int n0 = tn * BN + UN * h;
-      // rows and columns past the end are not stored: any scale will do
-      const float* sxp = p.x_scales + min(row0 + lane, p.M - 1);
-      const float* swp = p.w_scales + (size_t)min(n0 / 128, (p.N - 1) / 128) * p.G;
-      float2 acc[64];
-#pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
-      // a K block's scale is loaded two blocks ahead of its use: beside the
-      // tiles' loads a read of L2 can take longer than one block
-      float sx[2], sw[2];
+      row0 = tm * 256 + (int)rank * BM + 32 * q;
+      n0 = tn * BN + UN * h;
+      sxp = p.x_scales + min(row0 + lane, p.M - 1);
+      swp = p.w_scales + (size_t)min(n0 / 128, (p.N - 1) / 128) * p.G;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int kb = min(j, p.G - 1);
         sx[j] = __ldg(sxp + (size_t)kb * p.M);
         sw[j] = __ldg(swp + kb);
       }
+    };
+    bool ok = true;
+    uint32_t tl = 0;   // tiles done
+    open(pair);
+    for (int tile = pair; tile < num_tiles && ok; tile += npairs, ++tl) {
+      float2 acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
       // The sums of consecutive K blocks are read as one stream of 16-column
       // steps: the next step's load is in flight during this step's
       // multiply-adds, across blocks too. The next block's barrier is tested
@@ -299,10 +335,12 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       }
       if (!ok) break;
       // ---- output: 128 columns in pieces of 128 bytes a row
+      const int m = row0, nt = n0;
+      if (tile + npairs < num_tiles) open(tile + npairs);
       if (p.out_f32) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int n = n0 + 32 * c;
+          const int n = nt + 32 * c;
           uint8_t* buf = sm.out[e][c % kSlots];
           if (lane == 0) bulk_wait_read<kSlots - 1>();
           __syncwarp();
@@ -322,17 +360,17 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (row0 < p.M && n < p.N) tma_store_2d(&tm_y, buf, n, row0);
+            if (m < p.M && n < p.N) tma_store_2d(&tm_y, buf, n, m);
             bulk_commit();
           }
         }
       } else {
-        // both pieces, then one fence for the two copies
-        if (lane == 0) bulk_wait_read<0>();
-        __syncwarp();
+        // both pieces, then one fence; warp 2 issues the copies (a warp that
+        // issues its own waits 1000 cycles a tile for it)
+        if (tl > 0 && !warp_wait(&sm.out_free, (tl - 1) & 1, p.wait_ns, p.err)) { ok = false; break; }
 #pragma unroll
         for (int c = 0; c < kSlots; ++c) {
-          const int n = n0 + 64 * c;
+          const int n = nt + 64 * c;
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
             uint4 b8 = make_uint4(0u, 0u, 0u, 0u);
@@ -350,11 +388,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          if (row0 < p.M && n0 < p.N) tma_store_2d(&tm_y, sm.out[e][0], n0, row0);
-          if (row0 < p.M && n0 + 64 < p.N) tma_store_2d(&tm_y, sm.out[e][1], n0 + 64, row0);
-          bulk_commit();
-        }
+        if (lane == 0) mbar_arrive(&sm.out_ready[e]);
       }
     }
     if (lane == 0) bulk_wait<0>();
