@@ -55,6 +55,20 @@ __device__ __forceinline__ void mbar_arrive_if(bool on, uint32_t cluster_addr) {
       : "memory");
 }
 
+// Whether phase `parity` of `bar` has completed, without holding the warp until
+// it has (mbar_try_wait may).
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // two fp32 -> bf16x2 (round to nearest even); `lo` in bits 0..15
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;

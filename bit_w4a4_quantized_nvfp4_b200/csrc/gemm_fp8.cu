@@ -102,6 +102,15 @@ __device__ __forceinline__ void tile_at(int t, const Params& p, int& tm, int& tn
   tn = r / rows;
 }
 
+// kHold: the early test of the next block's barrier may hold the warp until the
+// barrier turns (try_wait) or only looks (test_wait). Looking is faster while a
+// pair has few K blocks to do (21.7 us against 23.5 at 1024 x 4096 x 4096, 59.7
+// against 62.3 at 4608 x 1024 x 9216); in long runs holding is (530 us against
+// 538 at 8192^3, 240 against 243 at 4608 x 4096 x 12288): the halves' drains then
+// fall into step. At 2048 x 4096 x 12288, 192 blocks a pair, both take 115 us.
+constexpr int kHoldBlocks = 256;
+
+template <bool kHold>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const __grid_constant__ CUtensorMap tm_y, const Params p) {
@@ -282,8 +291,8 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       // The sums of consecutive K blocks are read as one stream of 16-column
       // steps: the next step's load is in flight during this step's
       // multiply-adds, across blocks too. The next block's barrier is tested
-      // (not waited for) ahead, since a test takes some 150 cycles beside the
-      // MMAs' shared-memory reads. Two blocks a turn, so that accumulators and
+      // ahead, since a test takes some 150 cycles beside the MMAs' shared-memory
+      // reads. Two blocks a turn, so that accumulators and
       // barriers are fixed addresses: in the few instructions between two
       // blocks every one counts.
       if (!warp_wait(&sm.acc_full[h], ph[0], p.wait_ns, p.err)) break;
@@ -324,7 +333,9 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
               sx[j] = __ldg(sxp + (size_t)kn * p.M);
               sw[j] = __ldg(swp + kn);
             }
-            if (c == 4) ready = mbar_try_wait(&sm.acc_full[2 * (j ^ 1) + h], ph[j ^ 1]);
+            if (c == 4)
+              ready = kHold ? mbar_try_wait(&sm.acc_full[2 * (j ^ 1) + h], ph[j ^ 1])
+                            : mbar_test_wait(&sm.acc_full[2 * (j ^ 1) + h], ph[j ^ 1]);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               acc[8 * c + i] = __ffma2_rn(
@@ -432,9 +443,11 @@ cudaError_t launch_fp8_linear(const Fp8GemmArgs& a, cudaStream_t s) {
   p.err = a.err;
   p.wait_ns = a.wait_ns;
   const size_t smem = sizeof(Smem) + 1024;
-  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(gemm_fp8_kernel), (int)smem);
-  if (e != cudaSuccess) return e;
   const int tiles = p.tiles_m * p.tiles_n, pairs = a.num_sms / 2;
+  const long long blocks = (long long)((tiles + pairs - 1) / pairs) * p.G;   // K blocks of a pair
+  auto kern = blocks >= kHoldBlocks ? gemm_fp8_kernel<true> : gemm_fp8_kernel<false>;
+  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), (int)smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (tiles < pairs ? tiles : pairs));
   cfg.blockDim = dim3(kThreads);
@@ -445,7 +458,7 @@ cudaError_t launch_fp8_linear(const Fp8GemmArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, gemm_fp8_kernel, tm_a, tm_b, tm_y, p);
+  e = cudaLaunchKernelEx(&cfg, kern, tm_a, tm_b, tm_y, p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -351,12 +351,13 @@ cudaError_t launch_rows_t(const Fp8GemmArgs& a, int split, cudaStream_t s) {
 
 // The plan is the one with the least estimated time, in microseconds:
 //   this kernel     waves (a + c blocks) + 1.2 with a split
-//   the pair kernel 6.5 + waves (2 + 0.44 blocks)
+//   the pair kernel 5.2 + waves (1.7 + 0.41 blocks)
 // where a wave is one CTA (pair) per SM and blocks the K blocks of a CTA.
 // Measured at N = 4096 with 8, 32 and 64 blocks: T = 64 5.9, 12.3, 20.7 us
 // (a = 3.8, c = 0.265), T = 128 8.0, 15.6, 26.4 (5.4, 0.33), the pair kernel
-// 12.6, 23.4, 37.3; three waves of it at 32 blocks 54.4. So M = 512, N = K =
-// 4096 comes here (16.6 us against 23.9), M = 512 with N = 12288 does not.
+// 10.1, 20.3, 33.4; three waves of it at 8 and 32 blocks 19.3, 47.2. So M = 512,
+// N = K = 4096 comes here (16.6 us against 20.3), M = 512 with N = 12288 does not
+// (33.6 on the pair kernel, three waves here).
 // Up to 32 tokens the tile is as wide as they are and two CTAs fit on an SM,
 // but the second set is better left to the next launch, whose start it hides
 // (1 x 4096 x 9216: 144 CTAs 9.0 us, 288 11.9), unless a CTA's part of K is
@@ -378,7 +379,7 @@ bool fp8_rows_plan(const Fp8GemmArgs& a, int* tokens, int* split) {
     *split = S;
     return true;
   }
-  const double pair = 6.5 + (double)up(up(a.M, 256) * up(a.N, 256), a.num_sms / 2) * (2.0 + 0.44 * G);
+  const double pair = 5.2 + (double)up(up(a.M, 256) * up(a.N, 256), a.num_sms / 2) * (1.7 + 0.41 * G);
   double best = pair;
   for (int T : {64, 128}) {
     const long long tiles = tn * up(a.M, T);
