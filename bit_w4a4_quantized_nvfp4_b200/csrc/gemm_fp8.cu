@@ -29,20 +29,24 @@
 //     cycles beside the MMAs' shared-memory reads, an accumulator's way from
 //     the issuer through the drain and back several hundred. So a drain warp
 //     has one hand-over per K block (128 columns; units of 64 columns, two
-//     hand-overs, took 496 us at 8192^3, this 463), the next block's barrier is
-//     tested ahead, the issuers test both their barriers at once, and each half
-//     has its own issuer and its own two accumulators, so that one half's
-//     hand-over runs under the other's MMAs (one issuer with N = 256 products
-//     and two accumulators for both halves: 478 against 469).
-//   - Output straight from the registers, 32 bytes a store, was slower than
-//     the staging (522 us against 510 at 8192^3, 79 against 69 at 4608 x 1024 x
-//     9216): a thread's stores are rows apart.
-// Measured: 8192^3 463 us (2.37 PFLOP/s; the measured bf16 rate is 1.65 in
-// bursts, so 0.72 of twice that), 4608 x 4096 x 12288 208 us (2.23). Both run
-// into the 1000 W limit: at 463 us the SMs have gone down to 1.36 GHz, a copy
-// without the drain's arithmetic and loads takes 425 us at the same power, and
-// back to back for a second the same product takes 553 us (1.99 PFLOP/s, 1.44
-// times the bf16 rate under the same limit). What bounds it now is energy.
+//     hand-overs, took 496 us at 8192^3 where this took 463), the next block's
+//     barrier is tested ahead, the issuers test both their barriers at once, and
+//     each half has its own issuer and its own two accumulators, so that one
+//     half's hand-over runs under the other's MMAs (one issuer with N = 256
+//     products and two accumulators for both halves: 478 against 469).
+//   - A tile's end is short: the drain stages its columns and goes on, warp 2
+//     issues the copies (a warp waits 1000 cycles to issue its own), and the
+//     next tile's scales are loaded ahead (4608 x 1024 x 9216 with bias 62 us,
+//     58 so). Output straight from the registers, 32 bytes a store, was slower
+//     than the staging (522 us against 510 at 8192^3): a thread's stores are
+//     rows apart.
+// Measured: 8192^3 450 us (2.44 PFLOP/s; the measured bf16 rate is 1.65 in
+// bursts, so 0.74 of twice that), 4608 x 4096 x 12288 203 us (2.28), 1024 x 4096 x
+// 4096 20.3 us. The large ones run into the 1000 W limit: the SMs go down to 1.35
+// GHz, and back to back for a second 8192^3 takes 530 us (2.07 PFLOP/s, 1.5 times
+// the bf16 rate under the same limit). A copy of an earlier version (463 us)
+// without the drain's arithmetic and loads took 425 us at the same power: what
+// bounds it is energy, the operands' way to the SMs and the products themselves.
 #include "fp8.cuh"
 #include "kernels.h"
 
