@@ -76,6 +76,18 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return r;
 }
 
+// A wait that runs out sends its kernel to the end. What is in flight by then
+// (copies, MMAs, stores of the cluster's other CTAs into this one) has to land
+// before shared memory and tensor memory are given up. That takes microseconds
+// and has this limit of its own, however short the waits' limit was set.
+constexpr unsigned long long kLandNs = 100000000ull;
+
+// The same for copies whose barrier is another CTA's: a millisecond.
+__device__ __forceinline__ void let_copies_land() {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+}
+
 // Register shares of a warpgroup (all four warps execute it).
 template <int N>
 __device__ __forceinline__ void regs_inc() {

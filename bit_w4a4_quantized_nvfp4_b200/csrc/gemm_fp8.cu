@@ -180,13 +180,9 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
             tma_load_2d_pair(st + kABytes + kBBytes / 2, &tm_b, fb, kb * BK, col0 + UN);
           }
         }
-        if (!ok && leader) {
-          // let the copies already issued by both CTAs land before the pair exits
-          for (uint32_t d = 1; d <= (uint32_t)kStages && d <= it; ++d) {
-            const uint32_t j = it - d;
-            (void)mbar_wait(&sm.full[j % kStages], (j / kStages) & 1, p.wait_ns, nullptr);
-          }
-        }
+        // the copies already issued land before the pair exits (both CTAs'
+        // count on the leader's barriers, which the other cannot wait for)
+        if (!ok) let_copies_land();
       }
     } else if ((warp == 1 || warp == 3) && leader) {
       // ---------------------------------------------------------- MMA issuers
@@ -229,7 +225,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       // every MMA issued has completed before tensor memory is freed
       if (elect_one()) tc_commit_pair(&sm.mma_done, 0x1);
       __syncwarp();
-      (void)warp_wait(&sm.mma_done, 0, p.wait_ns, p.err);
+      (void)warp_wait(&sm.mma_done, 0, kLandNs, p.err);
     } else if (warp == 2 && !p.out_f32) {
       // ---------------------------------------------------------- output copies
       uint32_t tl = 0;

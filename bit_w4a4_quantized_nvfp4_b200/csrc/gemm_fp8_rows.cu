@@ -147,7 +147,7 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
       }
       if (!ok) {
         // let the copies already issued land before the CTA can exit
-        for (int j = max(0, k - S); j < k; ++j) (void)mbar_wait(&full[j % S], (j / S) & 1, p.wait_ns, nullptr);
+        for (int j = max(0, k - S); j < k; ++j) (void)mbar_wait(&full[j % S], (j / S) & 1, kLandNs, nullptr);
       }
     }
     __syncwarp();
@@ -187,7 +187,7 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
     // every MMA issued has completed before tensor memory is freed
     if (elect_one()) tc_commit(mma_done);
     __syncwarp();
-    (void)warp_wait(mma_done, 0, p.wait_ns, p.err);
+    (void)warp_wait(mma_done, 0, kLandNs, p.err);
   }
 
   constexpr int HT = C::kHT;
@@ -280,7 +280,10 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
                        mapa_shared(smem_u32(joined), to), acc[t / 2].x, acc[t / 2].y, acc[t / 2 + 1].x,
                        acc[t / 2 + 1].y);
       }
-    if (groups > 0 && __all_sync(0xffffffffu, mbar_wait_cluster(joined, 0, p.wait_ns, p.err)) && n < p.N) {
+    // (a CTA whose wait runs out stays until the others' late stores have come)
+    const bool whole = groups == 0 || mbar_wait_cluster(joined, 0, p.wait_ns, p.err);
+    if (!whole && !mbar_wait_cluster(joined, 0, p.wait_ns, nullptr)) (void)mbar_wait_cluster(joined, 0, kLandNs, nullptr);
+    if (groups > 0 && __all_sync(0xffffffffu, whole) && n < p.N) {
       for (int u = (warp - 2) / 4; u < groups; u += C::kDrainWarps / 4) {
         const int t = rank * per + 4 * u;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);

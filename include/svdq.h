@@ -280,7 +280,8 @@ svdq_status svdq_fp8_quantize_act(int M, int K, const uint16_t* x, long long ldx
  *      exactly when residual is. residual_out may be x or residual itself
  *      (same address and stride); any other overlap of an output with an
  *      input or another output gives SVDQ_ERR_INVALID_ARG.
- * Shapes: as svdq_fp8_quantize_act, K <= 32768 (a row is held in registers).
+ * Shapes: as svdq_fp8_quantize_act, K <= 32768 (the maxima of a row's blocks
+ * are held in shared memory).
  * Pointers 16-byte aligned. */
 svdq_status svdq_fp8_norm_quantize(int M, int K, const uint16_t* x, long long ldx, const uint16_t* residual,
                                    long long ldr, const uint16_t* weight, float eps, uint16_t* residual_out,
