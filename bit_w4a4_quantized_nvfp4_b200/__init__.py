@@ -463,31 +463,39 @@ class Fp8Weight:
     scales: torch.Tensor  # float32 [ceil(N/128), ceil(K/128)]
 
 
-_F8 = torch.float8_e4m3fn
+# (bound once: these calls are as short as the host makes them)
+_F8, _BF16, _F32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32
+_device, _empty_strided = torch.cuda.current_device, torch.empty_strided
 
 
 def _blocks(n: int) -> int:
     return (n + 127) // 128
 
 
-def _rows(t: torch.Tensor, name: str, cols: Optional[int] = None) -> int:
-    """Row stride (elements) of a bf16 [M, K] tensor whose rows may be a
-    column range of a wider tensor: unit column stride, and rows that follow
-    one another without overlap (a stride in a dimension of size one says
-    nothing and is not looked at)."""
-    if t.dtype is not torch.bfloat16 or t.dim() != 2:
+def _rows(t: torch.Tensor, name: str):
+    """(M, K, row stride in elements) of a bf16 [M, K] tensor whose rows may
+    be a column range of a wider tensor: unit column stride, and rows that
+    follow one another without overlap (a stride in a dimension of size one
+    says nothing and is not looked at)."""
+    if t.dtype is not _BF16 or t.dim() != 2:
         raise ValueError(f"{name}: expected bfloat16 [M, K]")
     M, K = t.shape
-    if cols is not None and K != cols:
-        raise ValueError(f"{name}: {K} columns, expected {cols}")
     s0, s1 = t.stride()
-    if K > 1 and s1 != 1:
+    if s1 != 1 and K > 1:
         raise ValueError(f"{name}: expected unit stride along the columns")
     if M <= 1:
-        return (K + 7) // 8 * 8
+        return M, K, (K + 7) // 8 * 8
     if s0 < K:
         raise ValueError(f"{name}: row stride {s0} is less than the row's {K} columns")
-    return s0
+    return M, K, s0
+
+
+def _rows_as(t: torch.Tensor, name: str, M: int, K: int) -> int:
+    """Row stride of such a tensor of M rows of K columns."""
+    m, k, ld = _rows(t, name)
+    if m != M or k != K:
+        raise ValueError(f"{name}: shape {(m, k)}, expected {(M, K)}")
+    return ld
 
 
 def _addr(t: torch.Tensor, dev: int, name: str) -> int:
@@ -511,37 +519,39 @@ def _flat(t: Optional[torch.Tensor], dev: int, name: str):
 def _current(t: torch.Tensor) -> int:
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
-    return torch.cuda.current_device()
+    return _device()
 
 
 def _new(rows: int, cols: int, dtype, device, stream) -> torch.Tensor:
     """A contiguous output [rows, cols] of a call on ``stream``, allocated for
     the stream that writes it (empty_strided takes two thirds of empty's time)."""
     if stream is None:
-        return torch.empty_strided((rows, cols), (max(cols, 1), 1), dtype=dtype, device=device)
+        return _empty_strided((rows, cols), (cols or 1, 1), dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty_strided((rows, cols), (max(cols, 1), 1), dtype=dtype, device=device)
+        return _empty_strided((rows, cols), (cols or 1, 1), dtype=dtype, device=device)
 
 
-def _fp8_act_out(out: Optional[Fp8Act], M: int, K: int, device, stream) -> Fp8Act:
+def _fp8_act_out(out: Optional[Fp8Act], M: int, K: int, x: torch.Tensor, stream, dev: int):
+    """(the Fp8Act of a call, the addresses of its codes and scales)"""
     G = (K + 127) // 128
     if out is None:
-        return Fp8Act(M, K, _new(M, K, _F8, device, stream), _new(G, M, torch.float32, device, stream))
-    _need(out.M == M and out.K == K, "out: Fp8Act of M {}, K {}", out.M, out.K)
+        device = x.device
+        codes, scales = _new(M, K, _F8, device, stream), _new(G, M, _F32, device, stream)
+        return Fp8Act(M, K, codes, scales), codes.data_ptr(), scales.data_ptr()
+    if out.M != M or out.K != K:
+        raise ValueError(f"out: Fp8Act of M {out.M}, K {out.K}")
     _is(out.codes, _F8, (M, K), "out.codes")
-    _is(out.scales, torch.float32, (G, M), "out.scales")
-    return out
+    _is(out.scales, _F32, (G, M), "out.scales")
+    return out, _flat(out.codes, dev, "out.codes"), _flat(out.scales, dev, "out.scales")
 
 
 def fp8_quantize_act(x: torch.Tensor, stream=None, out: Optional[Fp8Act] = None) -> Fp8Act:
     """svdq_fp8_quantize_act: x bf16 [M, K] (rows may be strided) -> codes, scales."""
-    ldx = _rows(x, "x")
-    M, K = x.shape
+    M, K, ldx = _rows(x, "x")
     dev = _current(x)
-    out = _fp8_act_out(out, M, K, x.device, stream)
-    _check("svdq_fp8_quantize_act", load().svdq_fp8_quantize_act(
-        M, K, _addr(x, dev, "x"), ldx, _flat(out.codes, dev, "out.codes"), _flat(out.scales, dev, "out.scales"),
-        _stream(stream, dev)))
+    px = _addr(x, dev, "x")
+    out, pc, ps = _fp8_act_out(out, M, K, x, stream, dev)
+    _check("svdq_fp8_quantize_act", load().svdq_fp8_quantize_act(M, K, px, ldx, pc, ps, _stream(stream, dev)))
     return out
 
 
@@ -551,29 +561,27 @@ def fp8_norm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float, residua
     RMSNorm(r) * weight. Returns (Fp8Act, r); r is None without a residual.
     x, residual and residual_out bf16 [M, K], rows may be strided;
     residual_out may be x or residual (in place)."""
-    ldx = _rows(x, "x")
-    M, K = x.shape
-    _is(weight, torch.bfloat16, (K,), "weight")
+    M, K, ldx = _rows(x, "x")
+    _is(weight, _BF16, (K,), "weight")
     dev = _current(x)
+    px, pw = _addr(x, dev, "x"), _flat(weight, dev, "weight")
     pr = po = None
     ldr = ldo = 0
     if residual is not None:
-        _need(residual.shape == x.shape, "residual: shape {}, x {}", residual.shape, x.shape)
-        ldr = _rows(residual, "residual")
+        ldr = _rows_as(residual, "residual", M, K)
         pr = _addr(residual, dev, "residual")
         if residual_out is None:
-            residual_out = _new(M, K, torch.bfloat16, x.device, stream)
+            residual_out = _new(M, K, _BF16, x.device, stream)
             ldo = (K + 7) // 8 * 8
+            po = residual_out.data_ptr()
         else:
-            _need(residual_out.shape == x.shape, "residual_out: shape {}, x {}", residual_out.shape, x.shape)
-            ldo = _rows(residual_out, "residual_out")
-        po = _addr(residual_out, dev, "residual_out")
-    else:
-        _need(residual_out is None, "residual_out given without residual")
-    out = _fp8_act_out(out, M, K, x.device, stream)
+            ldo = _rows_as(residual_out, "residual_out", M, K)
+            po = _addr(residual_out, dev, "residual_out")
+    elif residual_out is not None:
+        raise ValueError("residual_out given without residual")
+    out, pc, ps = _fp8_act_out(out, M, K, x, stream, dev)
     _check("svdq_fp8_norm_quantize", load().svdq_fp8_norm_quantize(
-        M, K, _addr(x, dev, "x"), ldx, pr, ldr, _flat(weight, dev, "weight"), float(eps), po, ldo,
-        _flat(out.codes, dev, "out.codes"), _flat(out.scales, dev, "out.scales"), _stream(stream, dev)))
+        M, K, px, ldx, pr, ldr, pw, float(eps), po, ldo, pc, ps, _stream(stream, dev)))
     return out, residual_out
 
 
@@ -599,25 +607,29 @@ def fp8_linear(qa: Fp8Act, w: Fp8Weight, bias: Optional[torch.Tensor] = None, ou
                out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """svdq_fp8_linear: y [M, N] = the product of the 8-bit operands, + bias. out_dtype "bf16" or "f32"."""
     M, K, N = qa.M, qa.K, w.N
-    _need(K == w.K, "activations have K = {}, the packed weight K = {}", K, w.K)
+    if K != w.K:
+        raise ValueError(f"activations have K = {K}, the packed weight K = {w.K}")
     _need(out_dtype == "bf16" or out_dtype == "f32", "out_dtype {!r}", out_dtype)
     G = (K + 127) // 128
-    _is(qa.codes, _F8, (M, K), "qa.codes")
-    _is(qa.scales, torch.float32, (G, M), "qa.scales")
-    _is(w.codes, _F8, (N, K), "w.codes")
-    _is(w.scales, torch.float32, ((N + 127) // 128, G), "w.scales")
+    xc, xs, wc, ws = qa.codes, qa.scales, w.codes, w.scales
+    _is(xc, _F8, (M, K), "qa.codes")
+    _is(xs, _F32, (G, M), "qa.scales")
+    _is(wc, _F8, (N, K), "w.codes")
+    _is(ws, _F32, ((N + 127) // 128, G), "w.scales")
     if bias is not None:
-        _is(bias, torch.bfloat16, (N,), "bias")
-    want = torch.bfloat16 if out_dtype == "bf16" else torch.float32
-    dev = _current(qa.codes)
+        _is(bias, _BF16, (N,), "bias")
+    want = _BF16 if out_dtype == "bf16" else _F32
+    dev = _current(xc)
+    pxc, pxs = _flat(xc, dev, "qa.codes"), _flat(xs, dev, "qa.scales")
+    pwc, pws, pb = _flat(wc, dev, "w.codes"), _flat(ws, dev, "w.scales"), _flat(bias, dev, "bias")
     if out is None:
-        out = _new(M, N, want, qa.codes.device, stream)
+        out = _new(M, N, want, xc.device, stream)
+        po = out.data_ptr()
     else:
         _is(out, want, (M, N), "out")
+        po = _flat(out, dev, "out")
     _check("svdq_fp8_linear", load().svdq_fp8_linear(
-        M, K, N, _flat(qa.codes, dev, "qa.codes"), _flat(qa.scales, dev, "qa.scales"), _flat(w.codes, dev, "w.codes"),
-        _flat(w.scales, dev, "w.scales"), _flat(bias, dev, "bias"), _flat(out, dev, "out"), _OUT[out_dtype],
-        _stream(stream, dev)))
+        M, K, N, pxc, pxs, pwc, pws, pb, po, _OUT[out_dtype], _stream(stream, dev)))
     return out
 
 
@@ -679,17 +691,18 @@ def rope_freqs(rot_dim, base: float = 10000.0, scaling: Optional[str] = None, fa
 
 def _rope_inputs(positions: torch.Tensor, freqs: RopeFreqs, dev: int):
     """(M, axes, pairs, pos, freq, axis) of a rotary call, checked."""
-    if positions.dtype is not torch.int64 or positions.dim() not in (1, 2):
+    shape = positions.shape
+    if positions.dtype is not torch.int64 or len(shape) not in (1, 2):
         raise ValueError("positions: expected int64 [M] or [M, axes]")
-    M, axes = positions.shape[0], 1 if positions.dim() == 1 else positions.shape[1]
-    f = freqs.freq
+    M, axes = shape if len(shape) == 2 else (shape[0], 1)
+    f, axis = freqs.freq, freqs.axis
     if f.dtype is not torch.float64 or f.dim() != 1:
         raise ValueError("freqs.freq: expected float64 [pairs]")
     pairs = f.shape[0]
-    if freqs.axis is not None:
-        _is(freqs.axis, torch.int32, (pairs,), "freqs.axis")
+    if axis is not None:
+        _is(axis, torch.int32, (pairs,), "freqs.axis")
     return (M, axes, pairs, _flat(positions, dev, "positions"), _flat(f, dev, "freqs.freq"),
-            _flat(freqs.axis, dev, "freqs.axis"))
+            _flat(axis, dev, "freqs.axis"))
 
 
 def rope_tables(positions: torch.Tensor, freqs: RopeFreqs, stream=None):
@@ -697,8 +710,8 @@ def rope_tables(positions: torch.Tensor, freqs: RopeFreqs, stream=None):
     [M, axes], the tables that pack_rope (pairs = 64) and qkv_norm_rope take."""
     dev = _current(positions)
     M, axes, pairs, pp, pf, pa = _rope_inputs(positions, freqs, dev)
-    cos = _new(M, pairs, torch.float32, positions.device, stream)
-    sin = _new(M, pairs, torch.float32, positions.device, stream)
+    device = positions.device
+    cos, sin = _new(M, pairs, _F32, device, stream), _new(M, pairs, _F32, device, stream)
     _check("svdq_rope_tables", load().svdq_rope_tables(M, axes, pairs, pp, pf, pa, float(freqs.factor),
                                                        cos.data_ptr(), sin.data_ptr(), _stream(stream, dev)))
     return cos, sin
@@ -712,21 +725,22 @@ def rope_apply(x: torch.Tensor, heads: int, head_dim: int, positions: torch.Tens
     first). In place unless ``out`` [M, heads * head_dim] is given; returns
     what was written to."""
     _need(layout in _ROPE_LAYOUT, "layout {!r}", layout)
-    ldx = _rows(x, "x")
+    rows, cols, ldx = _rows(x, "x")
     width = heads * head_dim
-    _need(heads >= 1 and head_dim >= 1 and x.shape[1] >= width, "x has {} columns, {} heads of {} need {}",
-          x.shape[1], heads, head_dim, width)
+    _need(heads >= 1 and head_dim >= 1 and cols >= width, "x has {} columns, {} heads of {} need {}",
+          cols, heads, head_dim, width)
     dev = _current(x)
+    px = _addr(x, dev, "x")
     M, axes, pairs, pp, pf, pa = _rope_inputs(positions, freqs, dev)
-    _need(M == x.shape[0], "positions: {} rows, x has {}", M, x.shape[0])
+    _need(M == rows, "positions: {} rows, x has {}", M, rows)
     if out is None:
-        out, ldy = x, ldx
+        out, py, ldy = x, px, ldx
     else:
-        ldy = _rows(out, "out", width)
-        _need(out.shape[0] == M, "out: {} rows, x has {}", out.shape[0], M)
+        ldy = _rows_as(out, "out", M, width)
+        py = _addr(out, dev, "out")
     _check("svdq_rope_apply", load().svdq_rope_apply(
-        M, heads, head_dim, pairs, _ROPE_LAYOUT[layout], axes, pp, pf, pa, float(freqs.factor), _addr(x, dev, "x"),
-        ldx, _addr(out, dev, "out"), ldy, _stream(stream, dev)))
+        M, heads, head_dim, pairs, _ROPE_LAYOUT[layout], axes, pp, pf, pa, float(freqs.factor), px, ldx, py, ldy,
+        _stream(stream, dev)))
     return out
 
 
