@@ -69,6 +69,13 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// `bytes` from p on into L2 (both multiples of 16). L2 is the point of coherence
+// of device memory: a prefetch ahead of the wait for the previous kernel can
+// never make a later load see an older value.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // two fp32 -> bf16x2 (round to nearest even); `lo` in bits 0..15
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;

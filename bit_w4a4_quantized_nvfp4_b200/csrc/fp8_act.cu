@@ -4,11 +4,11 @@
 //   r = bf16(x + residual);  v = r / sqrt(mean(r^2) + eps) * w
 //   per 128 columns: scale = max(max|v| / 448, 2^-126), code = e4m3(v / scale)
 // Bound by HBM: 3 bytes an element, 7 with a residual. Measured from HBM
-// (launches in a row): norm + residual 4608 x 4096 24.1 us, 5.5 TB/s, 0.85 of
-// the measured copy rate (20.4 us at that rate); 8192 x 8192 77.9 us, 0.93;
-// norm alone 4608 x 12288 33.0 us, 0.79; without the norm 4608 x 12288 27.6 us,
-// 0.95. What is left of the norm's is the columns' arithmetic (some ten instructions each)
-// and, at 4608 rows, one wave's start and end.
+// (launches in a row): norm + residual 4608 x 4096 22.9 us, 5.8 TB/s, 0.89 of
+// the measured copy rate (20.4 us at that rate); 8192 x 8192 77.1 us, 0.94;
+// norm alone 4608 x 12288 33.2 us, 0.79; without the norm 4608 x 12288 27.8 us,
+// 0.94. What is left of the norm's is the columns' arithmetic (some ten
+// instructions each) and, at 4608 rows, one wave's start and end.
 //
 // A lane holds 8 consecutive columns (16 bytes of bf16), so 16 lanes are one
 // block of 128: its largest magnitude is four shuffles. v stays in fp32 from
@@ -89,11 +89,19 @@ __global__ void __launch_bounds__(512, 2) fp8_norm_kernel(const Fp8ActArgs a, in
   const long long m = (long long)blockIdx.x * ((blockDim.x >> 5) / wpr) + mr;
   float* am_w = block_am + 2 * steps * warp;
   if (threadIdx.x == 0) launch_dependents();
+  // (the last CTA's rows past M take the barriers below and write nothing)
+  const bool live = m < a.M;
+  // Each row's first columns are on their way to L2 while the previous kernel
+  // ends (norm + residual 4608 x 4096 22.9 us, 24.0 without, 512 x 4096 4.4
+  // against 5.0; more than 2 KB a warp is slower at many rows).
+  if (tid == 0 && live) {
+    const uint32_t bytes = (uint32_t)min(2048 * wpr, 2 * a.K);
+    prefetch_l2(a.x + (size_t)m * (size_t)a.ldx, bytes);
+    if (RES) prefetch_l2(a.residual + (size_t)m * (size_t)a.ldr, bytes);
+  }
   // every input may be the previous kernel's output, every output may still
   // be read by it
   grid_dependency_wait();
-  // (the last CTA's rows past M take the barriers below and write nothing)
-  const bool live = m < a.M;
   const uint4* xp = reinterpret_cast<const uint4*>(a.x + (size_t)m * (size_t)a.ldx);
   const uint4* qp = reinterpret_cast<const uint4*>(a.residual + (size_t)m * (size_t)a.ldr);
   uint4* op = reinterpret_cast<uint4*>(a.residual_out + (size_t)m * (size_t)a.ldo);
@@ -207,13 +215,13 @@ __global__ void __launch_bounds__(512, 2) fp8_norm_kernel(const Fp8ActArgs a, in
 // -------------------------------------------------------------- no norm
 // Pieces of 256 columns a warp loads at once: two leave 30 registers, so the SM
 // is full of warps (4608 x 12288: 28.2 us; four 32.6, one 35.1). The row is read
-// once and marked so (27.6).
+// once and marked so (27.6). The wait for the previous kernel stands behind the
+// index arithmetic (512 x 4096 2.4 us, 2.6 ahead of it; 4608 x 12288 27.8, 27.5).
 constexpr int kPieces = 2;
 
 __global__ void __launch_bounds__(256) fp8_quant_kernel(const Fp8ActArgs a, int per_row, long long pieces) {
   const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) launch_dependents();
-  grid_dependency_wait();
   const long long p0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kPieces;
   // one division a thread (in 32 bits where the count allows), then steps
   long long r0 = pieces >> 31 ? p0 / per_row : (long long)((uint32_t)p0 / (uint32_t)per_row);
@@ -221,6 +229,7 @@ __global__ void __launch_bounds__(256) fp8_quant_kernel(const Fp8ActArgs a, int 
   uint4 x[kPieces];
   long long row[kPieces];
   int col[kPieces];
+  grid_dependency_wait();
 #pragma unroll
   for (int u = 0; u < kPieces; ++u) {
     row[u] = r0;

@@ -11,8 +11,8 @@
 // has a few rows (or, while rows are few, a piece of one), loads its first
 // columns, then forms its rows' cos and sin once in shared memory for all
 // heads, so the angles' arithmetic runs under the loads. Measured: 16384 rows of
-// 64 heads of 128, half layout, whole heads, 82.0 us (6.55 TB/s, the measured
-// copy rate); interleaved with half of each head rotated 87.1 us (0.95).
+// 64 heads of 128, half layout, whole heads, 78.5 us (6.8 TB/s, 1.06 of the
+// measured copy rate); interleaved with half of each head rotated 79.4 us.
 // Tables are bound by the functions' arithmetic: 65536 x 64 in 14.4 us.
 #include "fp8.cuh"
 #include "kernels.h"
@@ -64,9 +64,15 @@ __global__ void __launch_bounds__(256) rope_tables_kernel(const RopeArgs a, floa
 }
 
 constexpr int kThreadsO = 256;
-// Units a thread has in flight: two (interleaved 87.1 us at 16384 x 64 x 128,
-// in 40 registers; four 90.0 in 63, one 90.1).
+// Units a thread has in flight: two (16384 x 8 x 128 half 12.7 us, one 13.6,
+// four 16.0; 4096 x 128 heads interleaved 41.7, 43.7, 41.7), or one where a CTA
+// has a single row or piece without two for each thread (4608 x 48 x 128 half
+// 19.3 us against 20.3, 512 x 48 x 128 4.4 against 4.6).
 constexpr int kUnits = 2;
+// What of a row is brought to L2 ahead of its loads (16384 x 64 x 128 interleaved
+// 79.4 us, 87.8 without, half 78.5 against 82.7; 4096 x 128 heads 41.7 us, 43.0
+// with 16 KB; 64 KB makes 256 heads slower, 89 against 83).
+constexpr int kAheadBytes = 32 * 1024;
 constexpr int kMaxAngles = 4096;     // cos and sin of a CTA's rows (32 KB)
 
 // How a row is cut: `upr` units, head by head `uph` of them, the first `rot`
@@ -107,8 +113,8 @@ __device__ __forceinline__ float col(const uint32_t* r, int k) {
 }
 
 // V: columns of a load. Interleaved V = 8 (pairs past the last are passed
-// through); half V = 8, 4 or 1 as the number of pairs divides.
-template <bool HALF, int V>
+// through); half V = 8, 4 or 1 as the number of pairs divides. U: units in flight.
+template <bool HALF, int V, int U>
 __global__ void __launch_bounds__(kThreadsO) rope_apply_kernel(const RopeArgs a, const RopePlan pl) {
   extern __shared__ __align__(16) float turn[];   // [rows][pairs] cos, then sin
   const int P = a.pairs;
@@ -120,15 +126,19 @@ __global__ void __launch_bounds__(kThreadsO) rope_apply_kernel(const RopeArgs a,
   float* sn = turn + pl.rows * P;
   const bool inplace = a.x == a.y;
   if (threadIdx.x == 0) launch_dependents();
+  // rows of 1 KB or more (below, the prefetches cost more than they bring) are
+  // on their way to L2 while the previous kernel ends
+  if ((int)threadIdx.x < rows && pl.chunks == 1 && a.heads * a.head_dim >= 512)
+    prefetch_l2(a.x + (size_t)(m0 + threadIdx.x) * (size_t)a.ldx, (uint32_t)min(kAheadBytes, 2 * a.heads * a.head_dim));
   // every input may be the previous kernel's output, y may still be read by it
   grid_dependency_wait();
 
   bool angles = false;
-  for (int ub = u0; ub < u1; ub += kThreadsO * kUnits) {
-    uint32_t lo[kUnits][(V + 1) / 2], hi[kUnits][(V + 1) / 2];
-    int row[kUnits], col0[kUnits], unit[kUnits];
+  for (int ub = u0; ub < u1; ub += kThreadsO * U) {
+    uint32_t lo[U][(V + 1) / 2], hi[U][(V + 1) / 2];
+    int row[U], col0[U], unit[U];
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
+    for (int k = 0; k < U; ++k) {
       const int u = ub + k * kThreadsO + (int)threadIdx.x;
       unit[k] = -1;
       if (u >= u1) continue;
@@ -153,7 +163,7 @@ __global__ void __launch_bounds__(kThreadsO) rope_apply_kernel(const RopeArgs a,
       angles = true;
     }
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
+    for (int k = 0; k < U; ++k) {
       if (unit[k] < 0) continue;
       const float* c = cs + row[k] * P;
       const float* s = sn + row[k] * P;
@@ -274,10 +284,12 @@ cudaError_t launch_rope_apply(const RopeArgs& a, int num_sms, cudaStream_t s) {
   const long long grid = ((long long)a.M + pl.rows - 1) / pl.rows * pl.chunks;
   RopeArgs args = a;
   void* ptrs[] = {&args, &pl};
-  const void* fn = !a.half  ? reinterpret_cast<const void*>(rope_apply_kernel<false, 8>)
-                   : v == 8 ? reinterpret_cast<const void*>(rope_apply_kernel<true, 8>)
-                   : v == 4 ? reinterpret_cast<const void*>(rope_apply_kernel<true, 4>)
-                            : reinterpret_cast<const void*>(rope_apply_kernel<true, 1>);
+  const bool one = pl.chunks > 1 || (pl.rows == 1 && pl.upr < kThreadsO * kUnits);
+  auto pick = [&](auto two_units, auto one_unit) { return reinterpret_cast<const void*>(one ? one_unit : two_units); };
+  const void* fn = !a.half  ? pick(rope_apply_kernel<false, 8, kUnits>, rope_apply_kernel<false, 8, 1>)
+                   : v == 8 ? pick(rope_apply_kernel<true, 8, kUnits>, rope_apply_kernel<true, 8, 1>)
+                   : v == 4 ? pick(rope_apply_kernel<true, 4, kUnits>, rope_apply_kernel<true, 4, 1>)
+                            : pick(rope_apply_kernel<true, 1, kUnits>, rope_apply_kernel<true, 1, 1>);
   return launch_rope(fn, (unsigned)grid, pl.rows * P * 8, s, ptrs);
 }
 
