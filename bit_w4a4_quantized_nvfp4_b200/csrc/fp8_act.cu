@@ -4,9 +4,9 @@
 //   r = bf16(x + residual);  v = r / sqrt(mean(r^2) + eps) * w
 //   per 128 columns: scale = max(max|v| / 448, 2^-126), code = e4m3(v / scale)
 // Bound by HBM: 3 bytes an element, 7 with a residual. Measured from HBM
-// (launches in a row): norm + residual 4608 x 4096 22.9 us, 5.8 TB/s, 0.89 of
-// the measured copy rate (20.4 us at that rate); 8192 x 8192 77.1 us, 0.94;
-// norm alone 4608 x 12288 33.2 us, 0.79; without the norm 4608 x 12288 27.8 us,
+// (launches in a row): norm + residual 4608 x 4096 22.0 us, 6.0 TB/s, 0.93 of
+// the measured copy rate (20.4 us at that rate); 8192 x 8192 72.0 us, 1.01;
+// norm alone 4608 x 12288 33.0 us, 0.80; without the norm 4608 x 12288 27.8 us,
 // 0.94. What is left of the norm's is the columns' arithmetic (some ten
 // instructions each) and, at 4608 rows, one wave's start and end.
 //
@@ -92,8 +92,8 @@ __global__ void __launch_bounds__(512, 2) fp8_norm_kernel(const Fp8ActArgs a, in
   // (the last CTA's rows past M take the barriers below and write nothing)
   const bool live = m < a.M;
   // Each row's first columns are on their way to L2 while the previous kernel
-  // ends (norm + residual 4608 x 4096 22.9 us, 24.0 without, 512 x 4096 4.4
-  // against 5.0; more than 2 KB a warp is slower at many rows).
+  // ends (norm + residual 4608 x 4096, a row a warp, 22.9 us, 24.0 without; 512
+  // x 4096 4.4 against 5.0; more than 2 KB a warp is slower at many rows).
   if (tid == 0 && live) {
     const uint32_t bytes = (uint32_t)min(2048 * wpr, 2 * a.K);
     prefetch_l2(a.x + (size_t)m * (size_t)a.ldx, bytes);
@@ -282,12 +282,20 @@ cudaError_t launch_fp8_act(const Fp8ActArgs& a, int num_sms, cudaStream_t s) {
     return launch_pdl(reinterpret_cast<const void*>(fp8_quant_kernel), (unsigned)((pieces + 8 * kPieces - 1) / (8 * kPieces)),
                       256, 0, s, ptrs);
   }
-  // warps of a row: one where there are rows enough to fill the SMs (no
+  // Warps of a row: one where there are rows enough to fill the SMs (no
   // barrier, the least work beside the columns), more for fewer rows, but no
-  // more than the row has columns for
+  // more than the row has columns for. With a residual a warp has at most eight
+  // steps, unless more warps would leave lanes idle: memory takes few long
+  // streams better than many (4608 x 12288 60.5 us, 70.6 with a row a warp;
+  // 8192 x 8192 72.4 against 76.6; 4608 x 5120 27.1 with two warps, 28.2 with
+  // four). Without one it is the other way round (4608 x 12288 33.2, 35.9 with
+  // four warps a row).
   const int nv = a.K / 8;
+  auto lanes = [nv](int w) { return (nv + 64 * w - 1) / (64 * w) * 64 * w; };   // steps come in twos
   int wpr = 1;
-  while (wpr < 16 && (long long)a.M * wpr < 24ll * num_sms && wpr * 32 < nv) wpr *= 2;
+  while (wpr < 16 && wpr * 32 < nv &&
+         ((long long)a.M * wpr < 24ll * num_sms || (a.residual && nv > 8 * 32 * wpr && lanes(2 * wpr) <= lanes(wpr))))
+    wpr *= 2;
   const int warps = wpr < 8 ? 8 : wpr, rpc = warps / wpr;
   Fp8ActArgs args = a;
   float inv_k = (float)(1.0 / a.K);
