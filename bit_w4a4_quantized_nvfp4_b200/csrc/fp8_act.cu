@@ -4,20 +4,19 @@
 //   r = bf16(x + residual);  v = r / sqrt(mean(r^2) + eps) * w
 //   per 128 columns: scale = max(max|v| / 448, 2^-126), code = e4m3(v / scale)
 // Bound by HBM: 3 bytes an element, 7 with a residual. Measured from HBM
-// (launches in a row): norm + residual 4608 x 4096 22.0 us, 6.0 TB/s, 0.93 of
-// the measured copy rate (20.4 us at that rate); 8192 x 8192 72.0 us, 1.01;
-// norm alone 4608 x 12288 33.0 us, 0.80; without the norm 4608 x 12288 27.8 us,
-// 0.94. What is left of the norm's is the columns' arithmetic (some ten
-// instructions each) and, at 4608 rows, one wave's start and end.
+// (launches in a row): norm + residual 4608 x 4096 20.9 us, 6.3 TB/s, 0.98 of
+// the measured copy rate (20.4 us at that rate); 8192 x 8192 68.4 us; norm alone
+// 4608 x 12288 29.7 us, 0.89; without the norm 4608 x 12288 27.8 us, 0.95. What
+// is left of the norm's is the columns' arithmetic, some ten instructions each.
 //
-// A lane holds 8 consecutive columns (16 bytes of bf16), so 16 lanes are one
-// block of 128: its largest magnitude is four shuffles. v stays in fp32 from
-// the norm to its one rounding to E4M3 (no bf16 in between, which would round
-// twice); the residual's sum is rounded to bf16 first, since that is the
-// value the next layer reads.
+// A load is 8 consecutive columns (16 bytes of bf16); a block of 128 is 16 of
+// them, held by 16 lanes, or by 4 with four loads each: its largest magnitude is
+// four shuffles, or two. v stays in fp32 from the norm to its one rounding to
+// E4M3 (no bf16 in between, which would round twice); the residual's sum is
+// rounded to bf16 first, since that is the value the next layer reads.
 //
-// Norm: one pass, a row to a warp (to several while rows are few). Without the
-// norm blocks are independent: a warp takes two pieces of 256 columns at a time.
+// Norm: one pass, a row to a warp or several. Without the norm blocks are
+// independent: a warp takes two pieces of 256 columns at a time.
 #include "fp8.cuh"
 #include "kernels.h"
 
@@ -34,10 +33,11 @@ __device__ __forceinline__ float absmax8(const float2 (&v)[4]) {
   return absmax3(absmax3(v[0].x, v[0].y, v[1].x), absmax3(v[1].y, v[2].x, v[2].y), absmax3(v[3].x, v[3].y, 0.f));
 }
 
-// the same over the 16 lanes of a block (`lanes`: those that take part)
-__device__ __forceinline__ float block_max(float am, unsigned lanes = 0xffffffffu) {
+// the same over the LANES lanes of a block
+template <int LANES>
+__device__ __forceinline__ float block_max(float am) {
 #pragma unroll
-  for (int o = 8; o; o >>= 1) am = max_nan(am, __shfl_xor_sync(lanes, am, o));
+  for (int o = LANES / 2; o; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
   return am;
 }
 __device__ __forceinline__ float scale_of(float am) { return max_nan(am * (1.0f / 448.0f), kFp8MinScale); }
@@ -77,17 +77,22 @@ __device__ __forceinline__ void unpack8(const uint4 q, float2 (&v)[4]) {
 // max|t|. So one pass over the row writes r and the codes and leaves only
 // max|t| of each block behind; the scales follow once the row's sum is known,
 // and nothing of the row has to be held.
-// kAhead: vectors of 8 columns a thread has in flight
-template <bool RES, int kAhead>
+// A: vectors of 8 columns a thread has in flight. They belong to one block, so
+// 16 / A lanes share a block and its maximum and factor come once for all A
+// (norm alone 4608 x 12288 29.7 us; 33.0 with a block's vectors in 16 lanes).
+template <bool RES, int A>
 __global__ void __launch_bounds__(512, 2) fp8_norm_kernel(const Fp8ActArgs a, int wpr, float inv_k) {
+  constexpr int kLanes = 16 / A;
   __shared__ float part[2][16];
-  extern __shared__ float block_am[];   // [warps][2 * steps]
+  extern __shared__ float block_am[];   // [warps][2 A * steps]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int mr = warp / wpr, w0 = mr * wpr, tpr = 32 * wpr;
   const int tid = threadIdx.x - 32 * w0;
-  const int nv = a.K / 8, steps = (nv + tpr - 1) / tpr;
+  const int nv = a.K / 8, steps = (nv + A * tpr - 1) / (A * tpr);
   const long long m = (long long)blockIdx.x * ((blockDim.x >> 5) / wpr) + mr;
-  float* am_w = block_am + 2 * steps * warp;
+  float* am_w = block_am + 2 * A * steps * warp;
+  // this thread's vectors of a step: vector u of them is kLanes u further
+  auto at = [&](int j) { return ((j * wpr + warp - w0) * 2 * A + lane / kLanes) * 16 + lane % kLanes; };
   if (threadIdx.x == 0) launch_dependents();
   // (the last CTA's rows past M take the barriers below and write nothing)
   const bool live = m < a.M;
@@ -111,46 +116,58 @@ __global__ void __launch_bounds__(512, 2) fp8_norm_kernel(const Fp8ActArgs a, in
   float2 ss2 = make_float2(0.f, 0.f);
   float least = 0x1p127f;   // the smallest max|t| of a block that is not all zeros
   bool odd = false;         // a block whose products need the definition's order
-  for (int j0 = 0; j0 < steps; j0 += kAhead) {
-    uint4 r[kAhead], q[kAhead], w[kAhead];
+  for (int j = 0; j < steps; ++j) {
+    const int i0 = at(j);
+    uint4 r[A], q[A], w[A];
+    // whole steps (all but a row's last) load without conditions
+    const bool whole = live && (j * wpr + warp - w0 + 1) * 32 * A <= nv;
+    if (whole) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int i = (j0 + u) * tpr + tid;
-      const bool in = live && i < nv;
-      r[u] = in ? xp[i] : make_uint4(0u, 0u, 0u, 0u);
-      if (RES) q[u] = in ? qp[i] : make_uint4(0u, 0u, 0u, 0u);
-      w[u] = in ? __ldg(wp + i) : make_uint4(0u, 0u, 0u, 0u);
+      for (int u = 0; u < A; ++u) {
+        r[u] = xp[i0 + u * kLanes];
+        if (RES) q[u] = qp[i0 + u * kLanes];
+        w[u] = __ldg(wp + i0 + u * kLanes);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < A; ++u) {
+        const bool in = live && i0 + u * kLanes < nv;
+        r[u] = in ? xp[i0 + u * kLanes] : make_uint4(0u, 0u, 0u, 0u);
+        if (RES) q[u] = in ? qp[i0 + u * kLanes] : make_uint4(0u, 0u, 0u, 0u);
+        w[u] = in ? __ldg(wp + i0 + u * kLanes) : make_uint4(0u, 0u, 0u, 0u);
+      }
     }
+    float2 v[A][4];
+    float am = 0.f;
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int i = (j0 + u) * tpr + tid;
-      if (j0 + u >= steps) break;
-      float2 v[4], g[4];
-      unpack8(r[u], v);
+    for (int u = 0; u < A; ++u) {
+      float2 g[4];
+      unpack8(r[u], v[u]);
       if (RES) {
         unpack8(q[u], g);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = __fadd2_rn(v[k], g[k]);
-        r[u] = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
-                          pack_bf16x2(v[3].x, v[3].y));
-        unpack8(r[u], v);
+        for (int k = 0; k < 4; ++k) v[u][k] = __fadd2_rn(v[u][k], g[k]);
+        r[u] = make_uint4(pack_bf16x2(v[u][0].x, v[u][0].y), pack_bf16x2(v[u][1].x, v[u][1].y),
+                          pack_bf16x2(v[u][2].x, v[u][2].y), pack_bf16x2(v[u][3].x, v[u][3].y));
+        if (whole || (live && i0 + u * kLanes < nv)) op[i0 + u * kLanes] = r[u];
+        unpack8(r[u], v[u]);
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) ss2 = __ffma2_rn(v[k], v[k], ss2);
+      for (int k = 0; k < 4; ++k) ss2 = __ffma2_rn(v[u][k], v[u][k], ss2);
       unpack8(w[u], g);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = __fmul2_rn(v[k], g[k]);
-      const float am = block_max(absmax8(v));
-      const bool some = am != 0.f;
-      least = some ? fminf(least, am) : least;
-      odd = odd || (some && !(am >= 0x1p-100f && am < 0x1p127f));
-      const uint2 c = codes8(v, some ? 448.0f * rcp(am) : 0.f);
-      if (live && i < nv) {
-        if (RES) op[i] = r[u];
-        cp[i] = c;
-      }
-      if ((lane & 15) == 0) am_w[2 * (j0 + u) + (lane >> 4)] = am;
+      for (int k = 0; k < 4; ++k) v[u][k] = __fmul2_rn(v[u][k], g[k]);
+      am = max_nan(am, absmax8(v[u]));
     }
+    am = block_max<kLanes>(am);
+    const bool some = am != 0.f;
+    least = some ? fminf(least, am) : least;
+    odd = odd || (some && !(am >= 0x1p-100f && am < 0x1p127f));
+    const float f = some ? 448.0f * rcp(am) : 0.f;
+#pragma unroll
+    for (int u = 0; u < A; ++u)
+      if (whole || (live && i0 + u * kLanes < nv)) cp[i0 + u * kLanes] = codes8(v[u], f);
+    if (lane % kLanes == 0) am_w[2 * A * j + lane / kLanes] = am;
   }
   // the row's sum: lanes, then its warps (the same order whatever the timing)
   auto row_sum = [&](float s, float* buf) {
@@ -175,38 +192,49 @@ __global__ void __launch_bounds__(512, 2) fp8_norm_kernel(const Fp8ActArgs a, in
   if (ss > 0x1p120f || (ss < 0x1p-80f && a.eps < 0x1p-60f)) {
     up = ss > 0x1p120f ? 0x1p-64f : 0x1p64f;
     float s2 = 0.f;
-    for (int j = 0; j < steps; ++j) {
-      float2 v[4];
-      again(j * tpr + tid, v);
+    for (int j = 0; j < steps; ++j)
+      for (int u = 0; u < A; ++u) {
+        float2 v[4];
+        again(at(j) + u * kLanes, v);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        s2 = fmaf(up * v[k].x, up * v[k].x, s2);
-        s2 = fmaf(up * v[k].y, up * v[k].y, s2);
+        for (int k = 0; k < 4; ++k) {
+          s2 = fmaf(up * v[k].x, up * v[k].x, s2);
+          s2 = fmaf(up * v[k].y, up * v[k].y, s2);
+        }
       }
-    }
     ss = row_sum(s2, part[1]);
   }
   const float inv = up * rsqrtf(fmaf(ss, inv_k, up * a.eps * up));
   __syncwarp();
-  for (int l = lane; l < 2 * steps; l += 32) {
-    const int g = ((l >> 1) * tpr + (warp - w0) * 32 + 16 * (l & 1)) / 16;
+  for (int l = lane; l < 2 * A * steps; l += 32) {
+    const int g = (l / (2 * A) * wpr + warp - w0) * 2 * A + l % (2 * A);
     if (live && g * 16 < nv) a.scales[(size_t)g * a.M + m] = scale_of(am_w[l] * inv);
   }
   if (__any_sync(0xffffffffu, odd || least * inv * (1.0f / 448.0f) < kFp8MinScale)) {
     // the smallest scale, NaN, infinities, products r w out of fp32's range:
     // the warp's blocks by the definition, v first
     for (int j = 0; j < steps; ++j) {
-      const int i = j * tpr + tid;
-      float2 v[4], g[4];
-      again(i, v);
-      unpack8(i < nv ? __ldg(wp + i) : make_uint4(0u, 0u, 0u, 0u), g);
+      const int i0 = at(j);
+      float2 v[A][4];
+      float am = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = make_float2(v[k].x * inv * g[k].x, v[k].y * inv * g[k].y);
-      const float scale = scale_of(block_max(absmax8(v)));
-      const uint2 c = codes8(v, rcp(scale));
-      if (live && i < nv) {
-        cp[i] = c;
-        if ((lane & 15) == 0) a.scales[(size_t)(i / 16) * a.M + m] = scale;
+      for (int u = 0; u < A; ++u) {
+        float2 g[4];
+        const int i = i0 + u * kLanes;
+        again(i, v[u]);
+        unpack8(i < nv ? __ldg(wp + i) : make_uint4(0u, 0u, 0u, 0u), g);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[u][k] = make_float2(v[u][k].x * inv * g[k].x, v[u][k].y * inv * g[k].y);
+        am = max_nan(am, absmax8(v[u]));
+      }
+      const float scale = scale_of(block_max<kLanes>(am));
+#pragma unroll
+      for (int u = 0; u < A; ++u) {
+        const int i = i0 + u * kLanes;
+        if (live && i < nv) {
+          cp[i] = codes8(v[u], rcp(scale));
+          if (i % 16 == 0) a.scales[(size_t)(i / 16) * a.M + m] = scale;
+        }
       }
     }
   }
@@ -247,7 +275,7 @@ __global__ void __launch_bounds__(256) fp8_quant_kernel(const Fp8ActArgs a, int 
   for (int u = 0; u < kPieces; ++u) {
     float2 v[4];
     unpack8(x[u], v);
-    const float scale = scale_of(block_max(absmax8(v)));
+    const float scale = scale_of(block_max<16>(absmax8(v)));
     const uint2 c = codes8(v, rcp(scale));
     if (col[u] >= 0) {
       *reinterpret_cast<uint2*>(a.codes + (size_t)row[u] * a.K + col[u]) = c;
@@ -284,32 +312,35 @@ cudaError_t launch_fp8_act(const Fp8ActArgs& a, int num_sms, cudaStream_t s) {
   }
   // Warps of a row: one where there are rows enough to fill the SMs (no
   // barrier, the least work beside the columns), more for fewer rows, but no
-  // more than the row has columns for. With a residual a warp has at most eight
-  // steps, unless more warps would leave lanes idle: memory takes few long
-  // streams better than many (4608 x 12288 60.5 us, 70.6 with a row a warp;
-  // 8192 x 8192 72.4 against 76.6; 4608 x 5120 27.1 with two warps, 28.2 with
-  // four). Without one it is the other way round (4608 x 12288 33.2, 35.9 with
-  // four warps a row).
+  // more than the row has columns for. With a residual a thread has at most four
+  // vectors, unless more warps would leave lanes idle: memory takes few long
+  // streams better than many (8192 x 8192 68.4 us, 71.4 with eight, 76.6 with a
+  // row a warp; 4608 x 4096 20.9, 21.3, 23.2; 1200 x 8192 12.4 against 15.0; but
+  // 1024 x 8192 10.8 against 10.2). Without one it is the other way round (4608
+  // x 12288 29.7, 37.1 with eight).
   const int nv = a.K / 8;
   auto lanes = [nv](int w) { return (nv + 64 * w - 1) / (64 * w) * 64 * w; };   // steps come in twos
   int wpr = 1;
   while (wpr < 16 && wpr * 32 < nv &&
-         ((long long)a.M * wpr < 24ll * num_sms || (a.residual && nv > 8 * 32 * wpr && lanes(2 * wpr) <= lanes(wpr))))
+         ((long long)a.M * wpr < 24ll * num_sms || (a.residual && nv > 4 * 32 * wpr && lanes(2 * wpr) <= lanes(wpr))))
     wpr *= 2;
   const int warps = wpr < 8 ? 8 : wpr, rpc = warps / wpr;
   Fp8ActArgs args = a;
   float inv_k = (float)(1.0 / a.K);
   void* ptrs[] = {&args, &wpr, &inv_k};
-  const int steps = (nv + 32 * wpr - 1) / (32 * wpr);
-  // vectors in flight: four, but two where each brings the residual's along
-  // (in 64 registers four of those spill: 4608 x 4096 26.6 us against 24.1,
-  // 8192 x 8192 83.4 against 77.9; without a residual 13.1 against 14.1)
-  const void* fn = a.residual ? (steps < 2 ? reinterpret_cast<const void*>(fp8_norm_kernel<true, 1>)
-                                           : reinterpret_cast<const void*>(fp8_norm_kernel<true, 2>))
-                   : steps < 2 ? reinterpret_cast<const void*>(fp8_norm_kernel<false, 1>)
-                   : steps < 3 ? reinterpret_cast<const void*>(fp8_norm_kernel<false, 2>)
-                               : reinterpret_cast<const void*>(fp8_norm_kernel<false, 4>);
-  return launch_pdl(fn, (unsigned)(((long long)a.M + rpc - 1) / rpc), 32 * warps, warps * 2 * steps * 4, s, ptrs);
+  // Vectors in flight: four, two where each brings the residual's along (in 64
+  // registers four of those spill), fewer where the last step would be idle for
+  // more than an eighth.
+  auto padded = [&](int A) { return (nv + 32 * A * wpr - 1) / (32 * A * wpr) * (32 * A * wpr); };
+  int A = a.residual ? 2 : 4;
+  while (A > 1 && 8 * padded(A) > 9 * padded(1)) A /= 2;
+  const int steps = padded(A) / (32 * A * wpr);
+  const void* fn = a.residual ? (A == 1 ? reinterpret_cast<const void*>(fp8_norm_kernel<true, 1>)
+                                        : reinterpret_cast<const void*>(fp8_norm_kernel<true, 2>))
+                   : A == 1 ? reinterpret_cast<const void*>(fp8_norm_kernel<false, 1>)
+                   : A == 2 ? reinterpret_cast<const void*>(fp8_norm_kernel<false, 2>)
+                            : reinterpret_cast<const void*>(fp8_norm_kernel<false, 4>);
+  return launch_pdl(fn, (unsigned)(((long long)a.M + rpc - 1) / rpc), 32 * warps, warps * 2 * A * steps * 4, s, ptrs);
 }
 
 }  // namespace svdq
