@@ -118,6 +118,30 @@ def test_norm_quantize_extremes(M):
     assert (qa.codes[1].float() * plain.spread(qa.scales, K)[1]).isnan().all()   # 0 / 0
 
 
+@pytest.mark.parametrize("M,K,residual", [(3700, 7184, False), (3700, 2320, True), (40, 30736, False), (1300, 4112, True),
+                                          (9000, 1040, False), (300, 12304, True)])
+def test_norm_quantize_ragged(M, K, residual):
+    """Rows whose last step is short, in each number of loads in flight, with
+    rows that are summed again and blocks that are done again in between."""
+    x = _acts(M, K, M + K)
+    w = (1 + 0.2 * torch.randn(K, generator=_gen(2), device="cuda")).to(torch.bfloat16)
+    x[1] *= 1e-30
+    x[2] = 3.0e18
+    x[3, -144:] = 0.0
+    x[M - 1, :-16] *= 1e-3
+    w[K - 130] = 1e-38
+    w[-16:] = 1e30
+    res = torch.zeros_like(x) if residual else None
+    if residual:
+        res[5] = x[5]
+    qa, r = svdq.fp8_norm_quantize(x, w, 0.0, residual=res)
+    _ok()
+    v, r64 = plain.norm64(x, w, 0.0, res)
+    if residual:
+        assert torch.equal(r.view(torch.int16), r64.view(torch.int16))
+    plain.check_codes(qa.codes, qa.scales, v, NORM_DELTA)
+
+
 def test_quantize_extremes():
     """Without the norm a NaN or an infinity spoils its block of 128 alone."""
     x = _acts(4, 400, 4)
