@@ -72,6 +72,15 @@ def test_rope_apply(M, heads, D, rot, layout):
     assert torch.equal(x[:, :heads * D], y) and torch.equal(x[:, heads * D:], keep[:, heads * D:])
 
 
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("M,heads,D,rot", [(1300, 40, 128, 128), (1210, 96, 128, 64), (700, 300, 64, 64), (1300, 33, 72, 70),
+                                           (5000, 6, 128, 128), (2600, 12, 96, 48), (1190, 2, 1024, 1000)])
+def test_rope_many_wide_rows(M, heads, D, rot, layout):
+    """As above, at rows enough that each has a CTA of its own or shares one,
+    shorter and longer than a CTA takes at once."""
+    test_rope_apply(M, heads, D, rot, layout)
+
+
 @pytest.mark.parametrize("axes,rot", [((16, 56, 56), 128), ((2, 2), 4), ((8, 24), 32)])
 def test_axes_and_tables(axes, rot):
     """Several position axes; the tables against 64 bits, and the rotation by
