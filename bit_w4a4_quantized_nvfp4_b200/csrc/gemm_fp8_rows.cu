@@ -27,6 +27,9 @@ namespace {
 
 constexpr int kMaxSplit = 8;           // portable cluster size
 
+// Tokens of a tile that each CTA of a split adds, a multiple of 4.
+__host__ __device__ constexpr int join_tokens(int tile, int split) { return ((tile + split - 1) / split + 3) / 4 * 4; }
+
 template <int T>
 struct CfgR {
   static constexpr int kDrainWarps = T > 32 ? 8 : 4;
@@ -38,8 +41,14 @@ struct CfgR {
   static constexpr uint32_t kTmemCols = T * kBufs < 32 ? 32 : T * kBufs;
   static constexpr int kCtas = T <= 32 ? 2 : 1;   // CTAs per SM
   static constexpr int kScaleFloats = T <= 32 ? 4096 : 8192;   // scales of a CTA's part of K: blocks x T
-  // partial sums: split x the tokens a CTA adds (at least 4) x 128 rows
-  static constexpr int kRedBytes = (T > 4 * kMaxSplit ? T : 4 * kMaxSplit) * 128 * 4;
+  // partial sums: split x the tokens a CTA adds x 128 rows, at the worst split
+  static constexpr int red_tokens() {
+    int most = 0;
+    for (int s = 2; s <= kMaxSplit; s = T > 64 ? 2 * s : s + 1)   // at 128 tokens powers of two alone
+      most = s * join_tokens(T, s) > most ? s * join_tokens(T, s) : most;
+    return most;
+  }
+  static constexpr int kRedBytes = red_tokens() * 128 * 4;
   static constexpr int kFixed = kScaleFloats * 4 + kRedBytes + 512 + 1024;
   static constexpr int kFit = ((T <= 32 ? 113 : 226) * 1024 - kFixed) / kStageBytes;
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
@@ -93,7 +102,7 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
   const int tv = min(T, p.M - m0);            // tokens of the tile
   // With a split, CTA j of the cluster adds tokens j * per .. of the tile; all
   // its CTAs send it their sums of them, in groups of four tokens
-  const int per = max(T / p.split, 4);
+  const int per = join_tokens(T, p.split);
   const int groups = min(per / 4, (max(tv - rank * per, 0) + 3) / 4);   // this CTA's
 
   if (threadIdx.x == 0) {
@@ -352,7 +361,16 @@ cudaError_t launch_rows_t(const Fp8GemmArgs& a, int split, cudaStream_t s) {
 
 }  // namespace
 
-// The plan is the one with the least estimated time, in microseconds:
+// Of 148 SMs, those on which clusters of a size find room at one CTA an SM (a
+// cluster stays within a processing cluster of 16 to 20 SMs).
+constexpr int kRoom[kMaxSplit + 1] = {0, 148, 148, 135, 132, 130, 132, 105, 120};
+
+// Up to 32 tokens the tile is as wide as they are and two CTAs fit on an SM; K is
+// split as far as fills seven quarters of the SMs (5120 columns of K 4096, 40
+// tiles: split by 6 5.8 us, 3 6.2, 2 7.6, but 7, 280 CTAs, 7.9; 9216 columns: 3
+// 8.3, 2 8.9, 4, 288 CTAs, 10.9), while a CTA keeps four blocks (2048 x 4096, 16
+// blocks: 5 3.8 us, 8 4.4) or there is an SM for each (1024 x 1024: 8 2.6, 2 3.0).
+// Above, the plan is the one with the least estimated time, in microseconds:
 //   this kernel     waves (a + c blocks) + 1.2 with a split
 //   the pair kernel 5.2 + waves (1.7 + 0.41 blocks)
 // where a wave is one CTA (pair) per SM and blocks the K blocks of a CTA.
@@ -360,14 +378,8 @@ cudaError_t launch_rows_t(const Fp8GemmArgs& a, int split, cudaStream_t s) {
 // (a = 3.8, c = 0.265), T = 128 8.0, 15.6, 26.4 (5.4, 0.33), the pair kernel
 // 10.1, 20.3, 33.4; three waves of it at 8 and 32 blocks 19.3, 47.2. So M = 512,
 // N = K = 4096 comes here (16.6 us against 20.3), M = 512 with N = 12288 does not
-// (33.6 on the pair kernel, three waves here).
-// Up to 32 tokens the tile is as wide as they are and two CTAs fit on an SM,
-// but the second set is better left to the next launch, whose start it hides
-// (1 x 4096 x 9216: 144 CTAs 9.0 us, 288 11.9), unless a CTA's part of K is
-// long (16 x 12288 x 4096: 12 blocks on 256 CTAs 10.6 us, 24 on 128 11.9;
-// 1 x 4096 x 18432: 16 on 288 13.7, 32 on 144 15.1).
-// Clusters of 8 find room on about half of the SMs at one CTA each
-// (64 x 1024 x 2048: 8.5 us against 4.5 with clusters of 4).
+// (33.6 on the pair kernel, three waves here). Splits of any number help here too
+// (64 x 4096 x 5120: by 3 8.1 us, by 2 9.9; 77 x 2064 x 1000: by 6 4.9, by 4 5.2).
 bool fp8_rows_plan(const Fp8GemmArgs& a, int* tokens, int* split) {
   const int G = (a.K + 127) / 128;
   const long long tn = (a.N + 127) / 128;
@@ -375,8 +387,8 @@ bool fp8_rows_plan(const Fp8GemmArgs& a, int* tokens, int* split) {
   if (a.M <= 32) {
     const int T = a.M <= 16 ? 16 : 32;
     int S = 1;
-    while (S < kMaxSplit && 2 * S <= G && 2 * S * tn <= a.num_sms) S *= 2;
-    if (S < kMaxSplit && up(G, S) >= 24 && 2 * S * tn <= 2 * a.num_sms) S *= 2;
+    for (int t = 2; t <= kMaxSplit && t <= G; ++t)
+      if (4 * t * tn <= 7ll * a.num_sms && (up(G, t) >= 4 || t * tn <= a.num_sms)) S = t;
     if (up(G, S) * T > CfgR<16>::kScaleFloats) return false;
     *tokens = T;
     *split = S;
@@ -386,10 +398,9 @@ bool fp8_rows_plan(const Fp8GemmArgs& a, int* tokens, int* split) {
   double best = pair;
   for (int T : {64, 128}) {
     const long long tiles = tn * up(a.M, T);
-    for (int S = 1; S <= kMaxSplit && S <= G; S *= 2) {
-      if (S == 8 && tiles * S > a.num_sms / 2) break;
+    for (int S = 1; S <= kMaxSplit && S <= G; S = T > 64 ? 2 * S : S + 1) {
       if (up(G, S) * T > CfgR<64>::kScaleFloats || up(a.M, T) > 65535) continue;
-      const double blocks = (double)up(G, S), waves = (double)up(tiles * S, a.num_sms);
+      const double blocks = (double)up(G, S), waves = (double)up(tiles * S, (long long)a.num_sms * kRoom[S] / 148);
       const double t = waves * (T == 64 ? 3.8 + 0.265 * blocks : 5.4 + 0.33 * blocks) + (S > 1 ? 1.2 : 0.0);
       if (t < best) {
         best = t;

@@ -286,6 +286,17 @@ def test_linear_exact_sums(M, K, N):
     assert torch.equal(f.double(), y64)
 
 
+@pytest.mark.parametrize("M,K,N", [(1, 3600, 9216), (16, 3600, 4480), (7, 3600, 6400), (5, 2064, 5120), (3, 3600, 5120), (2, 640, 1024),
+                                   (32, 3600, 9216), (20, 3600, 4480), (31, 3600, 6400), (17, 2064, 5120), (18, 656, 8200),
+                                   (64, 4112, 5120), (77, 2064, 1000), (33, 4096, 2048), (100, 1552, 2560), (45, 1680, 3200),
+                                   (64, 1936, 1920), (130, 2064, 1000)])
+def test_linear_every_split(M, K, N):
+    """K in two to eight parts, whose sizes differ and whose tokens do not
+    divide evenly among those that add them."""
+    test_linear(M, K, N)
+    test_linear_exact_sums(M, K, N)
+
+
 @pytest.mark.parametrize("M", [1, 16, 40, 200])
 def test_linear_each_block_has_its_scale(M):
     """One block of K at a time carries a scale, the others 0: a scale taken
