@@ -88,23 +88,27 @@ __device__ __forceinline__ int div_magic(int u, unsigned long long magic) {
 }
 
 template <int N>
-__device__ __forceinline__ void load_cols(const uint16_t* p, uint32_t (&r)[(N + 1) / 2]) {
+__device__ __forceinline__ void load_cols(const uint16_t* p, uint32_t (&r)[4]) {
   if constexpr (N == 8) {
     const uint4 v = *reinterpret_cast<const uint4*>(p);
     r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
   } else if constexpr (N == 4) {
     const uint2 v = *reinterpret_cast<const uint2*>(p);
     r[0] = v.x; r[1] = v.y;
+  } else if constexpr (N == 2) {
+    r[0] = *reinterpret_cast<const uint32_t*>(p);
   } else {
     r[0] = *p;
   }
 }
 template <int N>
-__device__ __forceinline__ void store_cols(uint16_t* p, const uint32_t (&r)[(N + 1) / 2]) {
+__device__ __forceinline__ void store_cols(uint16_t* p, const uint32_t (&r)[4]) {
   if constexpr (N == 8)
     *reinterpret_cast<uint4*>(p) = make_uint4(r[0], r[1], r[2], r[3]);
   else if constexpr (N == 4)
     *reinterpret_cast<uint2*>(p) = make_uint2(r[0], r[1]);
+  else if constexpr (N == 2)
+    *reinterpret_cast<uint32_t*>(p) = r[0];
   else
     *p = (uint16_t)r[0];
 }
@@ -124,7 +128,6 @@ __global__ void __launch_bounds__(kThreadsO) rope_apply_kernel(const RopeArgs a,
   const int u0 = chunk * per, u1 = pl.chunks > 1 ? min(pl.upr, u0 + per) : rows * pl.upr;
   float* cs = turn;
   float* sn = turn + pl.rows * P;
-  const bool inplace = a.x == a.y;
   if (threadIdx.x == 0) launch_dependents();
   // rows of 1 KB or more (below, the prefetches cost more than they bring) are
   // on their way to L2 while the previous kernel ends
@@ -135,7 +138,7 @@ __global__ void __launch_bounds__(kThreadsO) rope_apply_kernel(const RopeArgs a,
 
   bool angles = false;
   for (int ub = u0; ub < u1; ub += kThreadsO * U) {
-    uint32_t lo[U][(V + 1) / 2], hi[U][(V + 1) / 2];
+    uint32_t lo[U][4], hi[U][4];
     int row[U], col0[U], unit[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
@@ -152,6 +155,10 @@ __global__ void __launch_bounds__(kThreadsO) rope_apply_kernel(const RopeArgs a,
       } else if (unit[k] < pl.rot) {
         load_cols<V>(xp + V * unit[k], lo[k]);
         load_cols<V>(xp + V * unit[k] + P, hi[k]);
+      } else if (pl.rw == 8) {   // (units past the rotated ones: not in place)
+        load_cols<8>(xp + 2 * P + 8 * (unit[k] - pl.rot), lo[k]);
+      } else {
+        load_cols<2>(xp + 2 * P + 2 * (unit[k] - pl.rot), lo[k]);
       }
     }
     if (!angles) {
@@ -217,13 +224,10 @@ __global__ void __launch_bounds__(kThreadsO) rope_apply_kernel(const RopeArgs a,
         }
         store_cols<V>(yp + p0, lo[k]);
         store_cols<V>(yp + p0 + P, hi[k]);
-      } else if (!inplace) {
-        const int at = 2 * P + pl.rw * (unit[k] - pl.rot);
-        const uint16_t* xp = a.x + (size_t)(m0 + row[k]) * (size_t)a.ldx + col0[k] + at;
-        if (pl.rw == 8)
-          *reinterpret_cast<uint4*>(yp + at) = *reinterpret_cast<const uint4*>(xp);
-        else
-          *reinterpret_cast<uint32_t*>(yp + at) = *reinterpret_cast<const uint32_t*>(xp);
+      } else if (pl.rw == 8) {
+        store_cols<8>(yp + 2 * P + 8 * (unit[k] - pl.rot), lo[k]);
+      } else {
+        store_cols<2>(yp + 2 * P + 2 * (unit[k] - pl.rot), lo[k]);
       }
     }
   }
