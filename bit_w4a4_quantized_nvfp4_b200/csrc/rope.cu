@@ -11,7 +11,7 @@
 // has a few rows (or, while rows are few, a piece of one), loads its first
 // columns, then forms its rows' cos and sin once in shared memory for all
 // heads, so the angles' arithmetic runs under the loads. Measured: 16384 rows of
-// 64 heads of 128, half layout, whole heads, 78.5 us (6.8 TB/s, 1.06 of the
+// 64 heads of 128, half layout, whole heads, 78.9 us (6.8 TB/s, 1.05 of the
 // measured copy rate); interleaved with half of each head rotated 79.4 us.
 // Tables are bound by the functions' arithmetic: 65536 x 64 in 14.4 us.
 #include "fp8.cuh"
@@ -70,18 +70,21 @@ constexpr int kThreadsO = 256;
 // 19.3 us against 20.3, 512 x 48 x 128 4.4 against 4.6).
 constexpr int kUnits = 2;
 // What of a row is brought to L2 ahead of its loads (16384 x 64 x 128 interleaved
-// 79.4 us, 87.8 without, half 78.5 against 82.7; 4096 x 128 heads 41.7 us, 43.0
+// 79.4 us, 87.8 without, half 78.9 against 82.7; 4096 x 128 heads 41.7 us, 43.0
 // with 16 KB; 64 KB makes 256 heads slower, 89 against 83).
 constexpr int kAheadBytes = 32 * 1024;
 constexpr int kMaxAngles = 4096;     // cos and sin of a CTA's rows (32 KB)
 
-// How a row is cut: `upr` units, head by head `uph` of them, the first `rot`
-// of a head rotated (interleaved: 8 columns of 4 pairs; half: V columns and
-// their partners), the rest, where they are copied, rw columns each.
+// How a row is cut into units: `uph` of each head (interleaved: 8 columns of 4
+// pairs each, those past the last pair passed through; half: `rot`, V columns
+// and their partners), then, half and not in place, `rest` of each head's other
+// columns, rw columns each. (Not head by head: a warp that had both kinds took
+// 96 us at 16384 x 64 x 128 with half of each head rotated, 81 so.)
 struct RopePlan {
   int rows, chunks;        // rows of a CTA; pieces of a row (one of the two is 1)
-  int upr, uph, rot, rw;
-  unsigned long long uph_magic, upr_magic;   // ceil(2^40 / d): u / d for u < 2^20
+  int upr, uph, rot, rest, rw;
+  int first;               // a row's units ahead of the rest's
+  unsigned long long uph_magic, upr_magic, rest_magic;   // ceil(2^40 / d): u / d for u < 2^20
 };
 __device__ __forceinline__ int div_magic(int u, unsigned long long magic) {
   return (int)(((unsigned long long)u * magic) >> 40);
@@ -146,8 +149,15 @@ __global__ void __launch_bounds__(kThreadsO) rope_apply_kernel(const RopeArgs a,
       unit[k] = -1;
       if (u >= u1) continue;
       row[k] = pl.chunks > 1 ? 0 : div_magic(u, pl.upr_magic);
-      const int ur = u - row[k] * pl.upr, h = div_magic(ur, pl.uph_magic);
-      unit[k] = ur - h * pl.uph;
+      const int ur = u - row[k] * pl.upr;
+      int h;
+      if (HALF && ur >= pl.first) {
+        h = div_magic(ur - pl.first, pl.rest_magic);
+        unit[k] = pl.rot + ur - pl.first - h * pl.rest;
+      } else {
+        h = div_magic(ur, pl.uph_magic);
+        unit[k] = ur - h * pl.uph;
+      }
       col0[k] = h * a.head_dim;
       const uint16_t* xp = a.x + (size_t)(m0 + row[k]) * (size_t)a.ldx + col0[k];
       if (!HALF) {
@@ -260,18 +270,21 @@ cudaError_t launch_rope_tables(const RopeArgs& a, float* cos_t, float* sin_t, in
 
 cudaError_t launch_rope_apply(const RopeArgs& a, int num_sms, cudaStream_t s) {
   const bool inplace = a.x == a.y;
-  const int P = a.pairs, rest = a.head_dim - 2 * P;
+  const int P = a.pairs;
   const int v = !a.half ? 8 : P % 8 == 0 ? 8 : P % 4 == 0 ? 4 : 1;
   RopePlan pl;
   pl.rw = (2 * P) % 8 == 0 ? 8 : 2;
   if (a.half) {
     pl.rot = P / v;
-    pl.uph = pl.rot + (inplace ? 0 : rest / pl.rw);
+    pl.uph = pl.rot;
+    pl.rest = inplace ? 0 : (a.head_dim - 2 * P) / pl.rw;
   } else {
+    pl.rest = 0;
     pl.rot = (2 * P + 7) / 8;
     pl.uph = inplace ? pl.rot : a.head_dim / 8;
   }
-  pl.upr = pl.uph * a.heads;
+  pl.first = pl.uph * a.heads;
+  pl.upr = pl.first + pl.rest * a.heads;
   // rows of a CTA: as many as give each thread its units, within the angles'
   // room, and no more than leave every SM four CTAs; where that is one row and
   // there are fewer rows than that, a row is cut into pieces of one unit a
@@ -284,6 +297,7 @@ cudaError_t launch_rope_apply(const RopeArgs& a, int num_sms, cudaStream_t s) {
   pl.chunks = spread < 1 ? (pl.upr + kThreadsO - 1) / kThreadsO : 1;
   if ((long long)a.M * pl.chunks > 8ll * num_sms) pl.chunks = 1;
   pl.uph_magic = ((1ull << 40) + pl.uph - 1) / pl.uph;
+  pl.rest_magic = pl.rest ? ((1ull << 40) + pl.rest - 1) / pl.rest : 0;
   pl.upr_magic = ((1ull << 40) + pl.upr - 1) / pl.upr;
   const long long grid = ((long long)a.M + pl.rows - 1) / pl.rows * pl.chunks;
   RopeArgs args = a;
