@@ -4,10 +4,11 @@
 //   r = bf16(x + residual);  v = r / sqrt(mean(r^2) + eps) * w
 //   per 128 columns: scale = max(max|v| / 448, 2^-126), code = e4m3(v / scale)
 // Bound by HBM: 3 bytes an element, 7 with a residual. Measured from HBM
-// (launches in a row): norm + residual 4608 x 4096 20.9 us, 6.3 TB/s, 0.98 of
-// the measured copy rate (20.4 us at that rate); 8192 x 8192 68.4 us; norm alone
-// 4608 x 12288 29.7 us, 0.89; without the norm 4608 x 12288 27.8 us, 0.95. What
-// is left of the norm's is the columns' arithmetic, some ten instructions each.
+// (launches in a row over three sets of inputs): norm + residual 4608 x 4096
+// 20.6 us, 6.4 TB/s, 0.99 of the measured copy rate (20.4 us at that rate); 8192
+// x 8192 67.8 us; norm alone 4608 x 12288 29.5 us, 0.89; without the norm 4608 x
+// 12288 28.2 us, 0.94. What is left of the norm's is the columns' arithmetic,
+// some ten instructions each.
 //
 // A load is 8 consecutive columns (16 bytes of bf16); a block of 128 is 16 of
 // them, held by 16 lanes, or by 4 with four loads each: its largest magnitude is
@@ -241,12 +242,12 @@ __global__ void __launch_bounds__(512, 2) fp8_norm_kernel(const Fp8ActArgs a, in
 }
 
 // -------------------------------------------------------------- no norm
-// Pieces of 256 columns a warp loads at once: two leave 30 registers, so the SM
-// is full of warps (4608 x 12288: 28.2 us; four 32.6, one 35.1). The row is read
-// once and marked so (27.6). The wait for the previous kernel stands behind the
-// index arithmetic (512 x 4096 2.4 us, 2.6 ahead of it; 4608 x 12288 27.8, 27.5).
-constexpr int kPieces = 2;
-
+// kPieces: pieces of 256 columns a warp loads at once. Two leave 30 registers, so
+// the SM is full of warps (4608 x 12288 28.2 us; one 35.1, four 33.3); with few
+// pieces one each (512 x 4096 2.1 us against 2.3, 800 x 4096 3.0 against 3.2, but
+// 1200 x 4096 4.3 against 3.9). The wait for the previous kernel stands behind
+// the index arithmetic (512 x 4096, two pieces: 2.4 us, 2.6 ahead of it).
+template <int kPieces>
 __global__ void __launch_bounds__(256) fp8_quant_kernel(const Fp8ActArgs a, int per_row, long long pieces) {
   const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) launch_dependents();
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(256) fp8_quant_kernel(const Fp8ActArgs a, int 
       c0 = 0;
       ++r0;
     }
-    x[u] = in ? __ldcs(reinterpret_cast<const uint4*>(a.x + (size_t)row[u] * (size_t)a.ldx + col[u]))
+    x[u] = in ? *reinterpret_cast<const uint4*>(a.x + (size_t)row[u] * (size_t)a.ldx + col[u])
               : make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
@@ -307,8 +308,10 @@ cudaError_t launch_fp8_act(const Fp8ActArgs& a, int num_sms, cudaStream_t s) {
     int per_row = (a.K + 255) / 256;
     long long pieces = (long long)a.M * per_row;
     void* ptrs[] = {&args, &per_row, &pieces};
-    return launch_pdl(reinterpret_cast<const void*>(fp8_quant_kernel), (unsigned)((pieces + 8 * kPieces - 1) / (8 * kPieces)),
-                      256, 0, s, ptrs);
+    const int n = pieces <= 96ll * num_sms ? 1 : 2;
+    const void* fn = n == 1 ? reinterpret_cast<const void*>(fp8_quant_kernel<1>)
+                            : reinterpret_cast<const void*>(fp8_quant_kernel<2>);
+    return launch_pdl(fn, (unsigned)((pieces + 8 * n - 1) / (8 * n)), 256, 0, s, ptrs);
   }
   // Warps of a row: one where there are rows enough to fill the SMs (no
   // barrier, the least work beside the columns), more for fewer rows, but no
