@@ -161,7 +161,7 @@ def test_binding_checks_rope(lib):
     x = _bf(8, 512)
     _raises("CUDA", svdq.rope_apply, x, 4, 128, pos, fr)                   # well formed
     _raises("5 heads", svdq.rope_apply, x, 5, 128, pos, fr)
-    _raises("layout", svdq.rope_apply, x, 4, 128, pos, fr, layout="neox")
+    _raises("layout", svdq.rope_apply, x, 4, 128, pos, fr, layout="split")
     _raises("x: expected", svdq.rope_apply, x.float(), 4, 128, pos, fr)
     _raises("CUDA", svdq.rope_tables, pos, fr)
 
