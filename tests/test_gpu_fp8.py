@@ -483,3 +483,47 @@ def test_block_of_a_transformer(M):
     plain.check_codes(qb.codes, qb.scales, v, NORM_DELTA)
     y64, mag = plain.linear64(qb.codes, qb.scales, wu.codes, wu.scales)
     assert ((u.double() - y64).abs() <= plain.linear_bound(mag, H)).all()
+
+
+@pytest.mark.parametrize("M", [1, 16, 64, 700])
+def test_captured_layers_give_the_bits_of_single_calls(M):
+    """Norm, linear, rotary in place, quantise, linear, three times over, each
+    on the previous one's output: a replayed graph, whose kernels start before
+    their predecessors end, against calls with a wait after each."""
+    D, F = 1024, 2560
+    pk = []
+    for i in range(3):
+        g = _gen(20 + i)
+        pk.append((svdq.fp8_pack_weight(torch.randn(D, F, generator=g, device="cuda") / 32),
+                   svdq.fp8_pack_weight(torch.randn(F, D, generator=g, device="cuda") / 50)))
+    w = torch.ones(D, device="cuda", dtype=torch.bfloat16)
+    fr, pos = svdq.rope_freqs(128), torch.arange(M, device="cuda") + 5
+
+    def layers(h, r, wait):
+        for a, b in pk:
+            qa, r = svdq.fp8_norm_quantize(h, w, 1e-6, residual=r, residual_out=r)
+            wait()
+            u = svdq.fp8_linear(qa, a)
+            wait()
+            svdq.rope_apply(u, F // 128, 128, pos, fr, layout="half")
+            wait()
+            qu = svdq.fp8_quantize_act(u)
+            wait()
+            h = svdq.fp8_linear(qu, b)
+            wait()
+        return h, r
+
+    sh, sr = _acts(M, D, 1), _acts(M, D, 2)
+    layers(sh, sr, lambda: None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        oh, orr = layers(sh, sr, lambda: None)
+    for it in range(20):
+        h, r = _acts(M, D, 100 + it), _acts(M, D, 200 + it)
+        sh.copy_(h)
+        sr.copy_(r)
+        graph.replay()
+        eh, er = layers(h, r, torch.cuda.synchronize)
+        _ok()
+        assert torch.equal(eh, oh) and torch.equal(er, orr)
