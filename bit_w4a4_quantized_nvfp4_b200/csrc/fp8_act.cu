@@ -189,9 +189,11 @@ __global__ void __launch_bounds__(512, 2) fp8_norm_kernel(const Fp8ActArgs a, in
   };
   float ss = row_sum(ss2.x + ss2.y, part[0]), up = 1.f;
   // squares of bf16 values can pass fp32's range at both ends: such a row is
-  // summed again, scaled by a power of two
+  // summed again, scaled by a power of two. Downwards by 2^80: 32768 squares of
+  // the largest value, 2^128, then add up to 2^111, and the columns that count
+  // in such a row, 2^52 and above, still have squares of 2^-56.
   if (ss > 0x1p120f || (ss < 0x1p-80f && a.eps < 0x1p-60f)) {
-    up = ss > 0x1p120f ? 0x1p-64f : 0x1p64f;
+    up = ss > 0x1p120f ? 0x1p-80f : 0x1p64f;
     float s2 = 0.f;
     for (int j = 0; j < steps; ++j)
       for (int u = 0; u < A; ++u) {

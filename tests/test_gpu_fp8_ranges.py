@@ -1,0 +1,66 @@
+"""The norm of the 8-bit layer at the ends of fp32's range, against 64 bits.
+
+bf16 values reach from 2^-133 to 2^128, so that a row's squares, its mean
+square's root and the products with the weight can each leave fp32 although the
+result lies within it."""
+
+import pytest
+import torch
+
+import bit_w4a4_quantized_nvfp4_b200 as svdq
+from tests import _plain as plain
+
+pytestmark = pytest.mark.gpu
+
+BF16_MAX = torch.finfo(torch.bfloat16).max
+# as for rows of ordinary size: a sum of up to 32768 squares (chains of at most
+# 128 + 20 additions), its mean, root and two products, under 2^8 roundings of
+# 2^-24 (one more where a factor is subnormal in fp32: it keeps 21 bits or more)
+NORM_DELTA = 2.0 ** -16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from bit_w4a4_quantized_nvfp4_b200 import build
+
+    build.build()
+    svdq.load()
+
+
+def _acts(M, K, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(M, K, generator=g, device="cuda").to(torch.bfloat16)
+
+
+def _norm(x, w, eps, residual):
+    """The kernel's codes and scales for x, split as x + 0 where residual is asked for."""
+    res = torch.zeros_like(x) if residual else None
+    qa, _ = svdq.fp8_norm_quantize(x, w, eps, residual=res)
+    torch.cuda.synchronize()
+    assert svdq.device_error() == 0
+    return qa
+
+
+# few rows (spread over several warps) and many (a row a warp), short and long
+SIZES = [(6, 16), (6, 400), (6, 4096), (5, 32768), (3700, 400)]
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("M,K", SIZES)
+def test_rows_at_the_top_of_the_range(M, K, residual):
+    """Rows whose sum of squares leaves fp32 however few of their columns are
+    large, up to a row of the largest bf16 value."""
+    x = _acts(M, K, K)
+    sign = torch.where(_acts(1, K, 1)[0] < 0, -1.0, 1.0)
+    x[0] = (1e37 * sign).to(torch.bfloat16)
+    x[1] = (2.5e38 * sign).to(torch.bfloat16)
+    x[2] = BF16_MAX
+    x[3, :] = 1.0
+    x[3, 3], x[3, -2] = 3e38, -3e38
+    x[4] = (x[4].float() * 2e18).to(torch.bfloat16)
+    w = (1 + 0.2 * _acts(1, K, 2)[0].float()).to(torch.bfloat16)
+    qa = _norm(x, w, 1e-6, residual)
+    v, _ = plain.norm64(x, w, 1e-6)
+    plain.check_codes(qa.codes, qa.scales, v, NORM_DELTA)
