@@ -191,9 +191,11 @@ __global__ void __launch_bounds__(512, 2) fp8_norm_kernel(const Fp8ActArgs a, in
   // squares of bf16 values can pass fp32's range at both ends: such a row is
   // summed again, scaled by a power of two. Downwards by 2^80: 32768 squares of
   // the largest value, 2^128, then add up to 2^111, and the columns that count
-  // in such a row, 2^52 and above, still have squares of 2^-56.
+  // in such a row, 2^52 and above, still have squares of 2^-56. Upwards by 2^80:
+  // the smallest value, 2^-133, squares to 2^-106, a sum below 2^-80 stays below
+  // 2^80, eps below 2^-60 below 2^100.
   if (ss > 0x1p120f || (ss < 0x1p-80f && a.eps < 0x1p-60f)) {
-    up = ss > 0x1p120f ? 0x1p-80f : 0x1p64f;
+    up = ss > 0x1p120f ? 0x1p-80f : 0x1p80f;
     float s2 = 0.f;
     for (int j = 0; j < steps; ++j)
       for (int u = 0; u < A; ++u) {
@@ -207,15 +209,17 @@ __global__ void __launch_bounds__(512, 2) fp8_norm_kernel(const Fp8ActArgs a, in
       }
     ss = row_sum(s2, part[1]);
   }
-  const float inv = up * rsqrtf(fmaf(ss, inv_k, up * a.eps * up));
+  const float root = rsqrtf(fmaf(ss, inv_k, up * a.eps * up)), inv = up * root;
   __syncwarp();
   for (int l = lane; l < 2 * A * steps; l += 32) {
     const int g = (l / (2 * A) * wpr + warp - w0) * 2 * A + l % (2 * A);
     if (live && g * 16 < nv) a.scales[(size_t)g * a.M + m] = scale_of(am_w[l] * inv);
   }
-  if (__any_sync(0xffffffffu, odd || least * inv * (1.0f / 448.0f) < kFp8MinScale)) {
-    // the smallest scale, NaN, infinities, products r w out of fp32's range:
-    // the warp's blocks by the definition, v first
+  if (__any_sync(0xffffffffu, odd || least * inv * (1.0f / 448.0f) < kFp8MinScale || inv > 0x1p100f)) {
+    // the smallest scale, NaN, infinities, products r w or a factor 1 / rms out
+    // of fp32's range: the warp's blocks by the definition, v first (in 64
+    // bits: of r, 1 / rms and w any two may leave fp32)
+    const double inv64 = (double)up * (double)root;
     for (int j = 0; j < steps; ++j) {
       const int i0 = at(j);
       float2 v[A][4];
@@ -227,7 +231,8 @@ __global__ void __launch_bounds__(512, 2) fp8_norm_kernel(const Fp8ActArgs a, in
         again(i, v[u]);
         unpack8(i < nv ? __ldg(wp + i) : make_uint4(0u, 0u, 0u, 0u), g);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[u][k] = make_float2(v[u][k].x * inv * g[k].x, v[u][k].y * inv * g[k].y);
+        for (int k = 0; k < 4; ++k)
+          v[u][k] = make_float2((float)(v[u][k].x * inv64 * g[k].x), (float)(v[u][k].y * inv64 * g[k].y));
         am = max_nan(am, absmax8(v[u]));
       }
       const float scale = scale_of(block_max<kLanes>(am));

@@ -64,3 +64,23 @@ def test_rows_at_the_top_of_the_range(M, K, residual):
     qa = _norm(x, w, 1e-6, residual)
     v, _ = plain.norm64(x, w, 1e-6)
     plain.check_codes(qa.codes, qa.scales, v, NORM_DELTA)
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("M,K", SIZES)
+def test_rows_at_the_bottom_of_the_range(M, K, residual):
+    """eps = 0 (or too small to count): rows of bf16 subnormals, whose inverse
+    root leaves fp32, one column among zeros, and weights that bring products
+    back to ordinary size."""
+    x = _acts(M, K, K + 1)
+    w = (1 + 0.2 * _acts(1, K, 2)[0].float()).to(torch.bfloat16)
+    x[0] = 2.0 ** -133
+    x[1] = (x[1].float() * 2.0 ** -128).to(torch.bfloat16)
+    x[2] = (x[2].float() * 2.0 ** -118).to(torch.bfloat16)
+    x[3] = 0.0
+    x[3, -1] = 2.0 ** -133
+    x[4] = (x[4].float() * 2.0 ** -50).to(torch.bfloat16)
+    for eps in (0.0, 2.0 ** -140):
+        qa = _norm(x, w, eps, residual)
+        v, _ = plain.norm64(x, w, eps)
+        plain.check_codes(qa.codes, qa.scales, v, NORM_DELTA)
