@@ -213,12 +213,14 @@ __global__ void __launch_bounds__(512, 2) fp8_norm_kernel(const Fp8ActArgs a, in
   __syncwarp();
   for (int l = lane; l < 2 * A * steps; l += 32) {
     const int g = (l / (2 * A) * wpr + warp - w0) * 2 * A + l % (2 * A);
-    if (live && g * 16 < nv) a.scales[(size_t)g * a.M + m] = scale_of(am_w[l] * inv);
+    const float top = am_w[l] * inv;   // max|v|
+    if (live && g * 16 < nv) a.scales[(size_t)g * a.M + m] = scale_of(top);
+    odd = odd || top > 0x1.fffffep127f;
   }
   if (__any_sync(0xffffffffu, odd || least * inv * (1.0f / 448.0f) < kFp8MinScale || inv > 0x1p100f)) {
-    // the smallest scale, NaN, infinities, products r w or a factor 1 / rms out
-    // of fp32's range: the warp's blocks by the definition, v first (in 64
-    // bits: of r, 1 / rms and w any two may leave fp32)
+    // the smallest scale, NaN, infinities, values, products r w or a factor
+    // 1 / rms out of fp32's range: the warp's blocks by the definition, v first
+    // (in 64 bits: of r, 1 / rms and w any two may leave fp32)
     const double inv64 = (double)up * (double)root;
     for (int j = 0; j < steps; ++j) {
       const int i0 = at(j);

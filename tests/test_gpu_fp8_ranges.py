@@ -84,3 +84,30 @@ def test_rows_at_the_bottom_of_the_range(M, K, residual):
         qa = _norm(x, w, eps, residual)
         v, _ = plain.norm64(x, w, eps)
         plain.check_codes(qa.codes, qa.scales, v, NORM_DELTA)
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("M,K", SIZES)
+def test_a_value_past_fp32_spoils_its_block(M, K, residual):
+    """Weights near the largest value: where r / rms * w leaves fp32 (r w stays
+    within) the block holds an infinity, so all of it stands for NaN; a block
+    that stays within is as ever, however near."""
+    x = (_acts(M, K, K + 2).float().clamp(-1.5, 1.5) / 64).to(torch.bfloat16)
+    x[:, 5] = 2.0 / 64
+    x[1] = 1.0 / 64
+    w = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    w[:8] = 3e38
+    if K > 256:
+        w[128:256] = 1e38
+    qa = _norm(x, w, 1e-6, residual)
+    v, _ = plain.norm64(x, w, 1e-6)
+    top = plain.scales64(v) * 448.0
+    limit = torch.finfo(torch.float32).max
+    gone = top > limit
+    # none of the inputs is within the norm's error of the border
+    assert ((top - limit).abs() > 1e-3 * limit).all() and gone[0, 0] and not gone[0, 1]
+    got = qa.codes.float() * plain.spread(qa.scales, K)
+    assert torch.equal(got.isnan(), plain.spread(gone, K))
+    rows = ~gone.any(0)
+    plain.check_codes(qa.codes[rows], qa.scales[:, rows], v[rows], NORM_DELTA)
+    assert (((qa.scales.double() - top / 448.0).abs() <= NORM_DELTA * top / 448.0) | gone).all()
