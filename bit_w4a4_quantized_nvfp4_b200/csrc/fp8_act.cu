@@ -215,7 +215,10 @@ __global__ void __launch_bounds__(512, 2) fp8_norm_kernel(const Fp8ActArgs a, in
     const int g = (l / (2 * A) * wpr + warp - w0) * 2 * A + l % (2 * A);
     const float top = am_w[l] * inv;   // max|v|
     if (live && g * 16 < nv) a.scales[(size_t)g * a.M + m] = scale_of(top);
-    odd = odd || top > 0x1.fffffep127f;
+    // Past fp32; or zeros that may be products r w below 2^-150, which count
+    // where 1 / rms brings them past the smallest code of the smallest scale,
+    // 2^-136 (so not in a row of zeros with an eps of 2^-26 or more)
+    odd = odd || top > 0x1.fffffep127f || (live && g * 16 < nv && am_w[l] == 0.f && inv > 0x1p13f);
   }
   if (__any_sync(0xffffffffu, odd || least * inv * (1.0f / 448.0f) < kFp8MinScale || inv > 0x1p100f)) {
     // the smallest scale, NaN, infinities, values, products r w or a factor

@@ -111,3 +111,26 @@ def test_a_value_past_fp32_spoils_its_block(M, K, residual):
     rows = ~gone.any(0)
     plain.check_codes(qa.codes[rows], qa.scales[:, rows], v[rows], NORM_DELTA)
     assert (((qa.scales.double() - top / 448.0).abs() <= NORM_DELTA * top / 448.0) | gone).all()
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("M,K", SIZES)
+def test_products_with_the_weight_below_fp32(M, K, residual):
+    """Small rows under small weights (eps = 0): r w rounds to zero in fp32
+    over a whole block while r / rms * w does not. Blocks of zeros beside them
+    stay zeros."""
+    x = _acts(M, K, K + 3)
+    w = (1 + 0.2 * _acts(1, K, 2)[0].float()).to(torch.bfloat16)
+    w[:128] = 2.0 ** -75
+    w[-16:] = 2.0 ** -132
+    x[0] = (x[0].float() * 2.0 ** -90).to(torch.bfloat16)
+    x[1] = (x[1].float() * 2.0 ** -30).to(torch.bfloat16)
+    x[2] = (x[2].float() * 2.0 ** -99).to(torch.bfloat16)
+    x[2, :8] = 0.0
+    if K > 256:
+        x[2, :256] = 0.0
+    qa = _norm(x, w, 0.0, residual)
+    v, _ = plain.norm64(x, w, 0.0)
+    plain.check_codes(qa.codes, qa.scales, v, NORM_DELTA)
+    if K > 256:
+        assert (qa.codes[2, :256].float() == 0).all() and (qa.scales[:2, 2] == plain.MIN_SCALE).all()
