@@ -225,6 +225,7 @@ __global__ void __launch_bounds__(512, 2) fp8_norm_kernel(const Fp8ActArgs a, in
     // 1 / rms out of fp32's range: the warp's blocks by the definition, v first
     // (in 64 bits: of r, 1 / rms and w any two may leave fp32)
     const double inv64 = (double)up * (double)root;
+    __syncwarp();   // the scales above, from other lanes, come before these
     for (int j = 0; j < steps; ++j) {
       const int i0 = at(j);
       float2 v[A][4];
