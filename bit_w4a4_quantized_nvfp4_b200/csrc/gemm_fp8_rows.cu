@@ -148,19 +148,18 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       int k = 0;
-      bool ok = true;
       for (; k < nkb; ++k) {
         const int s = k % S;
-        if (k >= S && !mbar_wait(&empty[s], ((k / S) - 1) & 1, p.wait_ns, p.err)) { ok = false; break; }
+        if (k >= S && !mbar_wait(&empty[s], ((k / S) - 1) & 1, p.wait_ns, p.err)) break;
         uint8_t* st = stages + s * C::kStageBytes;
         mbar_expect_tx(&full[s], C::kStageBytes);
         tma_load_2d(st, &tm_w, &full[s], (kb0 + k) * 128, n0);
         tma_load_2d(st + C::kWBytes, &tm_x, &full[s], (kb0 + k) * 128, m0);
       }
-      if (!ok) {
-        // let the copies already issued land before the CTA can exit
-        for (int j = max(0, k - S); j < k; ++j) (void)mbar_wait(&full[j % S], (j / S) & 1, kLandNs, nullptr);
-      }
+      // The copies issued land before the CTA can exit, whichever warp's wait ran
+      // out (the MMA warp may have left blocks that it never waited for; where
+      // none ran out they have landed by now)
+      for (int j = max(0, k - S); j < k; ++j) (void)mbar_wait(&full[j % S], (j / S) & 1, kLandNs, nullptr);
     }
     __syncwarp();
   } else if (warp == 1) {
