@@ -89,10 +89,10 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 // and has this limit of its own, however short the waits' limit was set.
 constexpr unsigned long long kLandNs = 100000000ull;
 
-// The same for copies whose barrier is another CTA's: a millisecond.
+// The same for copies whose barrier is another CTA's, which cannot be waited for.
 __device__ __forceinline__ void let_copies_land() {
   const uint64_t t0 = globaltimer_ns();
-  while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+  while (globaltimer_ns() - t0 < kLandNs) __nanosleep(1000);
 }
 
 // Register shares of a warpgroup (all four warps execute it).

@@ -180,8 +180,14 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
             tma_load_2d_pair(st + kABytes + kBBytes / 2, &tm_b, fb, kb * BK, col0 + UN);
           }
         }
-        // the copies already issued land before the pair exits (both CTAs'
-        // count on the leader's barriers, which the other cannot wait for)
+        // The copies issued land before the pair exits, whichever warp's wait ran
+        // out (the issuers may have left blocks that they never waited for). Both
+        // CTAs' count on the leader's barriers; a CTA that has stopped early
+        // leaves blocks without its half, which never turn them.
+        if (leader) {
+          for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
+            if (!mbar_wait(&sm.full[j % kStages], (j / kStages) & 1, kLandNs, nullptr)) break;
+        }
         if (!ok) let_copies_land();
       }
     } else if ((warp == 1 || warp == 3) && leader) {
