@@ -77,6 +77,10 @@ Span rows_span(const void* p, int rows, long long cols, long long ld, size_t ele
   return span(p, ((size_t)(rows - 1) * (size_t)ld + (size_t)cols) * elem);
 }
 bool overlap(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
+// The same rows (in place); the stride of a single row says nothing.
+bool same_rows(const void* a, long long lda, const void* b, long long ldb, int M) {
+  return a == b && (M == 1 || lda == ldb);
+}
 Span fp8_scale_span(const float* scales, int M, int K) {
   return span(scales, (size_t)((K + 127) / 128) * (size_t)M * sizeof(float));
 }
@@ -464,8 +468,8 @@ svdq_status svdq_fp8_norm_quantize(int M, int K, const uint16_t* x, long long ld
     const Span sr = rows_span(residual, M, K, ldr, 2), so = rows_span(residual_out, M, K, ldo, 2);
     if (overlap(sc, sr) || overlap(ss, sr) || overlap(so, sc) || overlap(so, ss) || overlap(so, sw))
       return SVDQ_ERR_INVALID_ARG;
-    if (overlap(so, sx) && !(residual_out == x && ldo == ldx)) return SVDQ_ERR_INVALID_ARG;
-    if (overlap(so, sr) && !(residual_out == residual && ldo == ldr)) return SVDQ_ERR_INVALID_ARG;
+    if (overlap(so, sx) && !same_rows(residual_out, ldo, x, ldx, M)) return SVDQ_ERR_INVALID_ARG;
+    if (overlap(so, sr) && !same_rows(residual_out, ldo, residual, ldr, M)) return SVDQ_ERR_INVALID_ARG;
   }
   int sms = 0;
   if ((st = device_info(nullptr, &sms)) != SVDQ_OK) return st;
@@ -542,7 +546,7 @@ svdq_status svdq_rope_apply(int M, int heads, int head_dim, int pairs, svdq_rope
   if (!aligned16(x) || !aligned16(y) || !aligned_to(pos, 8) || !aligned_to(freq, 8) || !aligned_to(axis, 4))
     return SVDQ_ERR_ALIGN;
   const Span sx = rows_span(x, M, width, ldx, 2), sy = rows_span(y, M, width, ldy, 2);
-  if (overlap(sx, sy) && !(x == y && ldx == ldy)) return SVDQ_ERR_INVALID_ARG;
+  if (overlap(sx, sy) && !same_rows(x, ldx, y, ldy, M)) return SVDQ_ERR_INVALID_ARG;
   if (rope_inputs_overlap(sy, M, axes, pairs, pos, freq, axis)) return SVDQ_ERR_INVALID_ARG;
   int sms = 0;
   svdq_status st = device_info(nullptr, &sms);

@@ -278,7 +278,7 @@ svdq_status svdq_fp8_quantize_act(int M, int K, const uint16_t* x, long long ldx
  *      weight bf16 [K]; eps >= 0.
  * Out: codes, scales; residual_out bf16 [M, K] (row stride ldo) = r, given
  *      exactly when residual is. residual_out may be x or residual itself
- *      (same address and stride); any other overlap of an output with an
+ *      (same address and, for more than one row, stride); any other overlap of an output with an
  *      input or another output gives SVDQ_ERR_INVALID_ARG.
  * Shapes: as svdq_fp8_quantize_act, K <= 32768 (the maxima of a row's blocks
  * are held in shared memory).
@@ -334,7 +334,7 @@ svdq_status svdq_rope_tables(int M, int axes, int pairs, const long long* pos, c
  * the columns past them unchanged. The Q and K sections of a grouped Q/K/V
  * row are adjacent, so one call with heads = query + key heads rotates both.
  * Out: y bf16 [M, heads * head_dim] (row stride ldy); y may be x itself (same
- *      address and stride: in place); any other overlap gives
+ *      address and, for more than one row, stride: in place); any other overlap gives
  *      SVDQ_ERR_INVALID_ARG.
  * Shapes: M >= 0 (M = 0 is a no-op), 1 <= pairs <= 512, 2 pairs <= head_dim,
  * head_dim % 8 == 0, heads * head_dim <= 2^20. x, y 16-byte aligned; the
