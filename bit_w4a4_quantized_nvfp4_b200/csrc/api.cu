@@ -77,6 +77,17 @@ Span rows_span(const void* p, int rows, long long cols, long long ld, size_t ele
   return span(p, ((size_t)(rows - 1) * (size_t)ld + (size_t)cols) * elem);
 }
 bool overlap(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
+// Rows of `cols` elements from a on at stride lda, and from b on at ldb. With
+// one stride they are column ranges of the same rows (the second starts d
+// columns after the first, counted round the row) and may lie side by side.
+bool rows_overlap(const void* a, long long lda, const void* b, long long ldb, int M, long long cols, size_t elem) {
+  if (!overlap(rows_span(a, M, cols, lda, elem), rows_span(b, M, cols, ldb, elem))) return false;
+  if (M == 1 || lda != ldb) return true;
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+  const uintptr_t row = (uintptr_t)lda * elem, len = (uintptr_t)cols * elem;
+  const uintptr_t d = pb >= pa ? (pb - pa) % row : (row - (pa - pb) % row) % row;
+  return d < len || d + len > row;
+}
 // The same rows (in place); the stride of a single row says nothing.
 bool same_rows(const void* a, long long lda, const void* b, long long ldb, int M) {
   return a == b && (M == 1 || lda == ldb);
@@ -468,8 +479,10 @@ svdq_status svdq_fp8_norm_quantize(int M, int K, const uint16_t* x, long long ld
     const Span sr = rows_span(residual, M, K, ldr, 2), so = rows_span(residual_out, M, K, ldo, 2);
     if (overlap(sc, sr) || overlap(ss, sr) || overlap(so, sc) || overlap(so, ss) || overlap(so, sw))
       return SVDQ_ERR_INVALID_ARG;
-    if (overlap(so, sx) && !same_rows(residual_out, ldo, x, ldx, M)) return SVDQ_ERR_INVALID_ARG;
-    if (overlap(so, sr) && !same_rows(residual_out, ldo, residual, ldr, M)) return SVDQ_ERR_INVALID_ARG;
+    if (rows_overlap(x, ldx, residual_out, ldo, M, K, 2) && !same_rows(residual_out, ldo, x, ldx, M))
+      return SVDQ_ERR_INVALID_ARG;
+    if (rows_overlap(residual, ldr, residual_out, ldo, M, K, 2) && !same_rows(residual_out, ldo, residual, ldr, M))
+      return SVDQ_ERR_INVALID_ARG;
   }
   int sms = 0;
   if ((st = device_info(nullptr, &sms)) != SVDQ_OK) return st;
@@ -545,8 +558,8 @@ svdq_status svdq_rope_apply(int M, int heads, int head_dim, int pairs, svdq_rope
   if (!pos || !freq || !x || !y) return SVDQ_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(y) || !aligned_to(pos, 8) || !aligned_to(freq, 8) || !aligned_to(axis, 4))
     return SVDQ_ERR_ALIGN;
-  const Span sx = rows_span(x, M, width, ldx, 2), sy = rows_span(y, M, width, ldy, 2);
-  if (overlap(sx, sy) && !same_rows(x, ldx, y, ldy, M)) return SVDQ_ERR_INVALID_ARG;
+  const Span sy = rows_span(y, M, width, ldy, 2);
+  if (rows_overlap(x, ldx, y, ldy, M, width, 2) && !same_rows(x, ldx, y, ldy, M)) return SVDQ_ERR_INVALID_ARG;
   if (rope_inputs_overlap(sy, M, axes, pairs, pos, freq, axis)) return SVDQ_ERR_INVALID_ARG;
   int sms = 0;
   svdq_status st = device_info(nullptr, &sms);

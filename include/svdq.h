@@ -259,7 +259,8 @@ svdq_status awq_w4a16_linear(int M, int K, int N, const uint16_t* x, const uint8
  * A block's scale is max(max|v| / 448, 2^-126), its codes e4m3(v / scale). A
  * block that holds a NaN or an infinity stands for NaN throughout.
  * Row strides (ldx, ...) are in elements, multiples of 8, at least the row's
- * length; they may exceed it (a column range of a wider tensor). */
+ * length; they may exceed it (a column range of a wider tensor; several
+ * arguments may be ranges of one tensor that share no column). */
 
 /* svdq_fp8_quantize_act — the 8-bit form of bf16 activations.
  * In:  x bf16 [M, K], row stride ldx. Out: codes, scales as above.
@@ -278,8 +279,8 @@ svdq_status svdq_fp8_quantize_act(int M, int K, const uint16_t* x, long long ldx
  *      weight bf16 [K]; eps >= 0.
  * Out: codes, scales; residual_out bf16 [M, K] (row stride ldo) = r, given
  *      exactly when residual is. residual_out may be x or residual itself
- *      (same address and, for more than one row, stride); any other overlap of an output with an
- *      input or another output gives SVDQ_ERR_INVALID_ARG.
+ *      (same address and, for more than one row, stride); any other overlap of
+ *      an output with an input or another output gives SVDQ_ERR_INVALID_ARG.
  * Shapes: as svdq_fp8_quantize_act, K <= 32768 (the maxima of a row's blocks
  * are held in shared memory).
  * Pointers 16-byte aligned. */

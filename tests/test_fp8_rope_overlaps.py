@@ -41,3 +41,23 @@ def test_one_row_in_place_whatever_the_strides(lib):
     # a part of the row is not the row
     assert rope(lib, 1, FAR, 512, FAR + 16, 512) is S.INVALID_ARG
     assert norm(lib, 1, FAR, 512, 2 * FAR, 1024, FAR + 16, 512) is S.INVALID_ARG
+
+
+def test_column_ranges_of_one_tensor(lib):
+    """Two column ranges of the same rows (one stride) that share no column do
+    not overlap; those that share one, or whose strides differ, do."""
+    for M in (1, 2, 9):
+        assert rope(lib, M, FAR, 1024, FAR + 2 * 256, 1024) in PASSED
+        assert rope(lib, M, FAR + 2 * 768, 1024, FAR, 1024) in PASSED
+        assert rope(lib, M, FAR, 1024, FAR + 2 * 248, 1024) is S.INVALID_ARG
+        assert rope(lib, M, FAR + 2 * 248, 1024, FAR, 1024) is S.INVALID_ARG
+        assert norm(lib, M, FAR, 1024, FAR + 2 * 256, 1024, FAR + 2 * 512, 1024) in PASSED
+        assert norm(lib, M, FAR, 1024, FAR + 2 * 256, 1024, FAR + 2 * 504, 1024) is S.INVALID_ARG
+        assert norm(lib, M, FAR + 2 * 512, 1024, FAR + 2 * 256, 1024, FAR + 2 * 264, 1024) is S.INVALID_ARG
+    # one range ends in the row after the one it starts in
+    assert rope(lib, 2, FAR, 1024, FAR + 2 * 776, 1024) is S.INVALID_ARG
+    assert rope(lib, 2, FAR, 1024, FAR + 2 * 768, 1024) in PASSED
+    # ranges a row apart, and rows of other strides in between
+    assert rope(lib, 2, FAR, 1024, FAR + 2 * (1024 + 256), 1024) in PASSED
+    assert rope(lib, 2, FAR, 1024, FAR + 2 * 1024, 1024) is S.INVALID_ARG
+    assert rope(lib, 4, FAR, 1024, FAR + 2 * 256, 2048) is S.INVALID_ARG

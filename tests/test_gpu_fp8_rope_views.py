@@ -56,3 +56,31 @@ def test_norm_in_place_through_views(M):
     _ok()
     assert torch.equal(r, s) and torch.equal(qa.codes.view(torch.uint8), qb.codes.view(torch.uint8))
     assert torch.equal(work[:, :256], wide[:, :256]) and torch.equal(work[:, 512:], wide[:, 512:])
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("M", [1, 3, 700])
+def test_rope_into_another_column_range(M, layout):
+    """From one column range of a tensor into another, nothing beside it written."""
+    fr = svdq.rope_freqs(64)
+    pos = torch.arange(M, device="cuda")
+    wide = _x(M, 1024, 4)
+    want = svdq.rope_apply(wide[:, :256].clone(), 2, 128, pos, fr, layout=layout)
+    work = wide.clone()
+    svdq.rope_apply(work[:, :256], 2, 128, pos, fr, layout=layout, out=work[:, 512:768])
+    _ok()
+    assert torch.equal(work[:, 512:768], want)
+    assert torch.equal(work[:, :512], wide[:, :512]) and torch.equal(work[:, 768:], wide[:, 768:])
+
+
+@pytest.mark.parametrize("M", [1, 3, 700])
+def test_norm_between_column_ranges(M):
+    """x, the residual and its output as three column ranges of one tensor."""
+    wide = _x(M, 1024, 5)
+    w = torch.ones(256, dtype=torch.bfloat16, device="cuda")
+    qa, r = svdq.fp8_norm_quantize(wide[:, :256].clone(), w, 1e-6, residual=wide[:, 256:512].clone())
+    work = wide.clone()
+    qb, s = svdq.fp8_norm_quantize(work[:, :256], w, 1e-6, residual=work[:, 256:512], residual_out=work[:, 768:])
+    _ok()
+    assert torch.equal(r, s) and torch.equal(qa.codes.view(torch.uint8), qb.codes.view(torch.uint8))
+    assert torch.equal(work[:, :768], wide[:, :768])
