@@ -472,6 +472,12 @@ def _blocks(n: int) -> int:
     return (n + 127) // 128
 
 
+def _sizes(a: int, b: int, c: int = 0) -> None:
+    """Sizes go to the library as C ints, which ctypes would wrap."""
+    if a > 0x7FFFFFFF or b > 0x7FFFFFFF or c > 0x7FFFFFFF:
+        raise ValueError(f"size {max(a, b, c)}: 2^31 - 1 is the largest")
+
+
 def _rows(t: torch.Tensor, name: str):
     """(M, K, row stride in elements) of a bf16 [M, K] tensor whose rows may
     be a column range of a wider tensor: unit column stride, and rows that
@@ -480,6 +486,7 @@ def _rows(t: torch.Tensor, name: str):
     if t.dtype is not _BF16 or t.dim() != 2:
         raise ValueError(f"{name}: expected bfloat16 [M, K]")
     M, K = t.shape
+    _sizes(M, K)
     s0, s1 = t.stride()
     if s1 != 1 and K > 1:
         raise ValueError(f"{name}: expected unit stride along the columns")
@@ -589,6 +596,7 @@ def fp8_pack_weight(W: torch.Tensor, stream=None, out: Optional[Fp8Weight] = Non
     """svdq_fp8_pack_weight: W fp32 [K, N] -> codes, scales (into ``out``'s buffers when given)."""
     _need(W.dim() == 2 and W.dtype == torch.float32, "W: expected float32 [K, N]")
     K, N = W.shape
+    _sizes(K, N)
     dev = _current(W)
     if out is None:
         out = Fp8Weight(K, N, _new(N, K, _F8, W.device, stream),
@@ -610,6 +618,7 @@ def fp8_linear(qa: Fp8Act, w: Fp8Weight, bias: Optional[torch.Tensor] = None, ou
     if K != w.K:
         raise ValueError(f"activations have K = {K}, the packed weight K = {w.K}")
     _need(out_dtype == "bf16" or out_dtype == "f32", "out_dtype {!r}", out_dtype)
+    _sizes(M, K, N)
     G = (K + 127) // 128
     xc, xs, wc, ws = qa.codes, qa.scales, w.codes, w.scales
     _is(xc, _F8, (M, K), "qa.codes")
@@ -689,8 +698,8 @@ def rope_freqs(rot_dim, base: float = 10000.0, scaling: Optional[str] = None, fa
     return RopeFreqs(torch.cat(parts).to(device), mult, axis)
 
 
-def _rope_inputs(positions: torch.Tensor, freqs: RopeFreqs, dev: int):
-    """(M, axes, pairs, pos, freq, axis) of a rotary call, checked."""
+def _rope_inputs(positions: torch.Tensor, freqs: RopeFreqs):
+    """(current device, M, axes, pairs, and the addresses of pos, freq, axis) of a rotary call, checked."""
     shape = positions.shape
     if positions.dtype is not torch.int64 or len(shape) not in (1, 2):
         raise ValueError("positions: expected int64 [M] or [M, axes]")
@@ -699,17 +708,18 @@ def _rope_inputs(positions: torch.Tensor, freqs: RopeFreqs, dev: int):
     if f.dtype is not torch.float64 or f.dim() != 1:
         raise ValueError("freqs.freq: expected float64 [pairs]")
     pairs = f.shape[0]
+    _sizes(M, axes, pairs)
     if axis is not None:
         _is(axis, torch.int32, (pairs,), "freqs.axis")
-    return (M, axes, pairs, _flat(positions, dev, "positions"), _flat(f, dev, "freqs.freq"),
+    dev = _current(positions)
+    return (dev, M, axes, pairs, _flat(positions, dev, "positions"), _flat(f, dev, "freqs.freq"),
             _flat(axis, dev, "freqs.axis"))
 
 
 def rope_tables(positions: torch.Tensor, freqs: RopeFreqs, stream=None):
     """svdq_rope_tables: (cos, sin) fp32 [M, pairs] at positions int64 [M] or
     [M, axes], the tables that pack_rope (pairs = 64) and qkv_norm_rope take."""
-    dev = _current(positions)
-    M, axes, pairs, pp, pf, pa = _rope_inputs(positions, freqs, dev)
+    dev, M, axes, pairs, pp, pf, pa = _rope_inputs(positions, freqs)
     device = positions.device
     cos, sin = _new(M, pairs, _F32, device, stream), _new(M, pairs, _F32, device, stream)
     _check("svdq_rope_tables", load().svdq_rope_tables(M, axes, pairs, pp, pf, pa, float(freqs.factor),
@@ -729,9 +739,8 @@ def rope_apply(x: torch.Tensor, heads: int, head_dim: int, positions: torch.Tens
     width = heads * head_dim
     _need(heads >= 1 and head_dim >= 1 and cols >= width, "x has {} columns, {} heads of {} need {}",
           cols, heads, head_dim, width)
-    dev = _current(x)
+    dev, M, axes, pairs, pp, pf, pa = _rope_inputs(positions, freqs)
     px = _addr(x, dev, "x")
-    M, axes, pairs, pp, pf, pa = _rope_inputs(positions, freqs, dev)
     _need(M == rows, "positions: {} rows, x has {}", M, rows)
     if out is None:
         out, py, ldy = x, px, ldx

@@ -1,6 +1,7 @@
 // C-ABI entry points (include/svdq.h): argument validation on the host, the
 // device-capability gate, tensor-map encoding and kernel launches.
 #include <atomic>
+#include <climits>
 #include <cstring>
 #include <mutex>
 
@@ -101,10 +102,14 @@ bool rope_inputs_overlap(const Span& out, int M, int axes, int pairs, const long
          (axis && overlap(out, span(axis, (size_t)pairs * 4)));
 }
 
+// Largest M, N and K of the 8-bit layer: blocks of up to 256 rows or columns are
+// counted in 32 bits.
+constexpr int kFp8MaxSize = INT_MAX - 255;
+
 // Sizes of an 8-bit activation call: M rows of K columns at row stride ld.
 svdq_status check_fp8_act(int M, int K, long long ld) {
   if (M < 0 || K <= 0) return SVDQ_ERR_INVALID_ARG;
-  if (K % 16 || ld < K || ld % 8) return SVDQ_ERR_SHAPE;
+  if (M > kFp8MaxSize || K > kFp8MaxSize || K % 16 || ld < K || ld % 8) return SVDQ_ERR_SHAPE;
   return SVDQ_OK;
 }
 
@@ -492,7 +497,7 @@ svdq_status svdq_fp8_norm_quantize(int M, int K, const uint16_t* x, long long ld
 
 svdq_status svdq_fp8_pack_weight(int K, int N, const float* W, uint8_t* codes, float* scales, void* stream) {
   if (K <= 0 || N <= 0) return SVDQ_ERR_INVALID_ARG;
-  if (K % 16 || N % 8 || N > (1 << 23) - 128) return SVDQ_ERR_SHAPE;
+  if (K > kFp8MaxSize || K % 16 || N % 8 || N > (1 << 23) - 128) return SVDQ_ERR_SHAPE;
   if (!W || !codes || !scales) return SVDQ_ERR_INVALID_ARG;
   if (!aligned16(W) || !aligned16(codes) || !aligned16(scales)) return SVDQ_ERR_ALIGN;
   svdq_status st = device_info(nullptr, nullptr);
@@ -504,7 +509,7 @@ svdq_status svdq_fp8_linear(int M, int K, int N, const uint8_t* x_codes, const f
                             const uint8_t* w_codes, const float* w_scales, const uint16_t* bias, void* y,
                             svdq_out_dtype out, void* stream) {
   if (M < 0 || K <= 0 || N <= 0) return SVDQ_ERR_INVALID_ARG;
-  if (K % 16 || N % 8) return SVDQ_ERR_SHAPE;
+  if (M > kFp8MaxSize || K > kFp8MaxSize || N > kFp8MaxSize || K % 16 || N % 8) return SVDQ_ERR_SHAPE;
   if (out != SVDQ_OUT_BF16 && out != SVDQ_OUT_F32) return SVDQ_ERR_INVALID_ARG;
   if (M == 0) return SVDQ_OK;
   if (!x_codes || !x_scales || !w_codes || !w_scales || !y) return SVDQ_ERR_INVALID_ARG;
