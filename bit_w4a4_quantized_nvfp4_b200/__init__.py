@@ -688,7 +688,8 @@ def rope_freqs(rot_dim, base: float = 10000.0, scaling: Optional[str] = None, fa
             def pair(turns):
                 return d * math.log(original_len / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
             lo, hi = max(math.floor(pair(32.0)), 0), min(math.ceil(pair(1.0)), d - 1)
-            slow = ((i - lo) / max(hi - lo, 0.001)).clamp(0.0, 1.0)
+            # (no ramp where not even the first pair turns once, or all turn 32 times)
+            slow = ((i - lo) / (hi - lo)).clamp(0.0, 1.0) if hi > lo else (i >= hi).to(torch.float64)
             f = f / factor * slow + f * (1.0 - slow)
             mult = 0.1 * math.log(factor) + 1.0
         parts.append(f)
