@@ -323,6 +323,8 @@ template <int T>
 cudaError_t launch_rows_t(const Fp8GemmArgs& a, int split, cudaStream_t s) {
   using C = CfgR<T>;
   static_assert(C::kStages >= 3 && (2 * C::kStages + 2 * C::kBufs + 3) * 8 <= 512, "shared-memory plan");
+  // (228 KB on an SM, 1 KB of it taken by each CTA)
+  static_assert(C::kSmem + kProbeMmaSmem > 226 * 1024, "no SM shared with the tensor-core probe");
   CUtensorMap tm_w, tm_x;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
   if (!make_tmap_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w_codes, a.K, a.N, a.K, 128, 128, sw) ||

@@ -157,6 +157,11 @@ cudaError_t launch_rope_tables(const RopeArgs& a, float* cos_t, float* sin_t, in
 cudaError_t launch_probe_convert(const float* in, long long n, uint8_t* e2m1, uint8_t* e4m3,
                                  uint16_t* bf16, cudaStream_t s);
 cudaError_t launch_probe_wait(unsigned* err, unsigned long long limit_ns, cudaStream_t s);
+// Shared memory of a probe CTA: so much that no CTA that takes tensor memory
+// shares its SM (those of gemm_fp8_rows.cu are the smallest). The probe takes
+// all columns of two SMs, and clusters whose CTAs crossed with its pairs would
+// each wait for the other's.
+constexpr int kProbeMmaSmem = 200 * 1024;
 cudaError_t launch_probe_mma(int iters, int mode, int num_sms, unsigned* err, unsigned long long wait_ns,
                              cudaStream_t s);
 

@@ -135,11 +135,8 @@ probe_mma_kernel(int iters, int mode, unsigned* err, unsigned long long wait_ns)
 
 cudaError_t launch_probe_mma(int iters, int mode, int num_sms, unsigned* err, unsigned long long wait_ns,
                              cudaStream_t s) {
-  // More than half of an SM's shared memory, so that no two CTAs share an SM:
-  // every pair takes all 512 tensor-memory columns, and two pairs whose CTAs
-  // crossed over two SMs would each wait for the other's columns.
-  const size_t smem = 120 * 1024;
-  static_assert(kPStage + 1024 <= 120 * 1024, "one stage fits");
+  const size_t smem = kProbeMmaSmem;
+  static_assert(kPStage + 1024 <= kProbeMmaSmem, "one stage fits");
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(probe_mma_kernel), (int)smem);
   if (e != cudaSuccess) return e;
   probe_mma_kernel<<<2 * (num_sms / 2), 128, smem, s>>>(iters, mode, err, wait_ns);
