@@ -33,7 +33,8 @@ __all__ = [
     "w4a4_linear_qkv", "qkv_norm_rope", "RopeTable", "pack_rope", "svdq_linear", "awq_pack_weight", "awq_w4a16_linear",
     "Fp8Act", "Fp8Weight", "fp8_quantize_act", "fp8_norm_quantize", "fp8_pack_weight", "fp8_linear",
     "RopeFreqs", "rope_freqs", "rope_tables", "rope_apply", "device_error", "set_wait_limit_ns",
-    "probe_convert", "probe_wait_timeout", "probe_mma_peak", "debug_force_arch",
+    "probe_convert", "probe_wait_timeout", "probe_mma_peak", "probe_fp8_linear_plan", "probe_fp8_act_plan",
+    "debug_force_arch",
 ]
 
 NVFP4, INT4 = 0, 1
@@ -90,6 +91,8 @@ SIGNATURES = {
     "svdq_set_wait_limit_ns": (None, [_U64]),
     "svdq_probe_convert": (_I, [_P, _I64, _P, _P, _P, _P]),
     "svdq_probe_wait_timeout": (_I, [_U64, _P]),
+    "svdq_probe_fp8_linear_plan": (_I, [_I, _I, _I, _I, _P]),
+    "svdq_probe_fp8_act_plan": (_I, [_I, _I, _I, _I, _I, _P]),
     "svdq_debug_force_arch": (None, [_I, _I]),
     "svdq_probe_mma_peak": (_I, [_I, _I, _P]),
 }
@@ -789,6 +792,20 @@ def probe_mma_peak(iters: int, mode: int = 0, stream=None) -> float:
     _check("svdq_probe_mma_peak", load().svdq_probe_mma_peak(int(iters), int(mode), _stream(stream)))
     sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
     return float(sms // 2) * iters * 4 * 2.0 * 256 * 256 * 64
+
+
+def probe_fp8_linear_plan(M: int, K: int, N: int, sms: int):
+    """(tokens of a tile, parts of K) that svdq_fp8_linear takes for few rows, (256, long run) for many."""
+    plan = (C.c_int * 2)()
+    _check("svdq_probe_fp8_linear_plan", load().svdq_probe_fp8_linear_plan(M, K, N, sms, plan))
+    return tuple(plan)
+
+
+def probe_fp8_act_plan(M: int, K: int, norm: bool, residual: bool, sms: int):
+    """(loads in flight, warps of a row) that the 8-bit activation pass takes."""
+    plan = (C.c_int * 2)()
+    _check("svdq_probe_fp8_act_plan", load().svdq_probe_fp8_act_plan(M, K, int(norm), int(residual), sms, plan))
+    return tuple(plan)
 
 
 def debug_force_arch(major: int, minor: int = 0) -> None:

@@ -531,6 +531,30 @@ svdq_status svdq_fp8_linear(int M, int K, int N, const uint8_t* x_codes, const f
   return from_cuda(launch_fp8_linear(a, static_cast<cudaStream_t>(stream)));
 }
 
+svdq_status svdq_probe_fp8_linear_plan(int M, int K, int N, int sms, int plan[2]) {
+  if (M < 1 || K <= 0 || N <= 0 || sms < 2 || !plan) return SVDQ_ERR_INVALID_ARG;
+  if (M > kFp8MaxSize || K > kFp8MaxSize || N > kFp8MaxSize || K % 16 || N % 8) return SVDQ_ERR_SHAPE;
+  Fp8GemmArgs a{};
+  a.M = M; a.K = K; a.N = N;
+  a.num_sms = sms;
+  if (!fp8_rows_plan(a, &plan[0], &plan[1])) {
+    plan[0] = 256;
+    plan[1] = fp8_pair_holds(a) ? 1 : 0;
+  }
+  return SVDQ_OK;
+}
+
+svdq_status svdq_probe_fp8_act_plan(int M, int K, int norm, int residual, int sms, int plan[2]) {
+  if (M < 1 || sms < 1 || !plan || (residual && !norm)) return SVDQ_ERR_INVALID_ARG;
+  const svdq_status st = check_fp8_act(M, K, K);
+  if (st != SVDQ_OK) return st;
+  if (norm && K > kFp8NormMaxK) return SVDQ_ERR_SHAPE;
+  const Fp8ActPlan pl = fp8_act_plan(M, K, norm != 0, residual != 0, sms);
+  plan[0] = pl.loads;
+  plan[1] = pl.warps;
+  return SVDQ_OK;
+}
+
 svdq_status svdq_rope_tables(int M, int axes, int pairs, const long long* pos, const double* freq, const int* axis,
                              float factor, float* cos_t, float* sin_t, void* stream) {
   if (M < 0 || axes < 1 || axes > 8 || pairs < 1) return SVDQ_ERR_INVALID_ARG;

@@ -315,16 +315,10 @@ cudaError_t launch_pdl(const void* fn, unsigned grid, int block, int smem, cudaS
 
 }  // namespace
 
-cudaError_t launch_fp8_act(const Fp8ActArgs& a, int num_sms, cudaStream_t s) {
-  if (!a.weight) {
-    Fp8ActArgs args = a;
-    int per_row = (a.K + 255) / 256;
-    long long pieces = (long long)a.M * per_row;
-    void* ptrs[] = {&args, &per_row, &pieces};
-    const int n = pieces <= 96ll * num_sms ? 1 : 2;
-    const void* fn = n == 1 ? reinterpret_cast<const void*>(fp8_quant_kernel<1>)
-                            : reinterpret_cast<const void*>(fp8_quant_kernel<2>);
-    return launch_pdl(fn, (unsigned)((pieces + 8 * n - 1) / (8 * n)), 256, 0, s, ptrs);
+Fp8ActPlan fp8_act_plan(int M, int K, bool norm, bool residual, int num_sms) {
+  if (!norm) {
+    const long long pieces = (long long)M * ((K + 255) / 256);
+    return Fp8ActPlan{pieces <= 96ll * num_sms ? 1 : 2, 1, 1};
   }
   // Warps of a row: one where there are rows enough to fill the SMs (no
   // barrier, the least work beside the columns), more for fewer rows, but no
@@ -334,29 +328,44 @@ cudaError_t launch_fp8_act(const Fp8ActArgs& a, int num_sms, cudaStream_t s) {
   // row a warp; 4608 x 4096 20.9, 21.3, 23.2; 1200 x 8192 12.4 against 15.0; but
   // 1024 x 8192 10.8 against 10.2). Without one it is the other way round (4608
   // x 12288 29.7, 37.1 with eight).
-  const int nv = a.K / 8;
+  const int nv = K / 8;
   auto lanes = [nv](int w) { return (nv + 64 * w - 1) / (64 * w) * 64 * w; };   // steps come in twos
   int wpr = 1;
   while (wpr < 16 && wpr * 32 < nv &&
-         ((long long)a.M * wpr < 24ll * num_sms || (a.residual && nv > 4 * 32 * wpr && lanes(2 * wpr) <= lanes(wpr))))
+         ((long long)M * wpr < 24ll * num_sms || (residual && nv > 4 * 32 * wpr && lanes(2 * wpr) <= lanes(wpr))))
     wpr *= 2;
-  const int warps = wpr < 8 ? 8 : wpr, rpc = warps / wpr;
-  Fp8ActArgs args = a;
-  float inv_k = (float)(1.0 / a.K);
-  void* ptrs[] = {&args, &wpr, &inv_k};
   // Vectors in flight: four, two where each brings the residual's along (in 64
   // registers four of those spill), fewer where the last step would be idle for
   // more than an eighth.
   auto padded = [&](int A) { return (nv + 32 * A * wpr - 1) / (32 * A * wpr) * (32 * A * wpr); };
-  int A = a.residual ? 2 : 4;
+  int A = residual ? 2 : 4;
   while (A > 1 && 8 * padded(A) > 9 * padded(1)) A /= 2;
-  const int steps = padded(A) / (32 * A * wpr);
+  return Fp8ActPlan{A, wpr, padded(A) / (32 * A * wpr)};
+}
+
+cudaError_t launch_fp8_act(const Fp8ActArgs& a, int num_sms, cudaStream_t s) {
+  const Fp8ActPlan pl = fp8_act_plan(a.M, a.K, a.weight != nullptr, a.residual != nullptr, num_sms);
+  Fp8ActArgs args = a;
+  if (!a.weight) {
+    int per_row = (a.K + 255) / 256;
+    long long pieces = (long long)a.M * per_row;
+    void* ptrs[] = {&args, &per_row, &pieces};
+    const int n = pl.loads;
+    const void* fn = n == 1 ? reinterpret_cast<const void*>(fp8_quant_kernel<1>)
+                            : reinterpret_cast<const void*>(fp8_quant_kernel<2>);
+    return launch_pdl(fn, (unsigned)((pieces + 8 * n - 1) / (8 * n)), 256, 0, s, ptrs);
+  }
+  int wpr = pl.warps;
+  const int A = pl.loads, warps = wpr < 8 ? 8 : wpr, rpc = warps / wpr;
+  float inv_k = (float)(1.0 / a.K);
+  void* ptrs[] = {&args, &wpr, &inv_k};
   const void* fn = a.residual ? (A == 1 ? reinterpret_cast<const void*>(fp8_norm_kernel<true, 1>)
                                         : reinterpret_cast<const void*>(fp8_norm_kernel<true, 2>))
                    : A == 1 ? reinterpret_cast<const void*>(fp8_norm_kernel<false, 1>)
                    : A == 2 ? reinterpret_cast<const void*>(fp8_norm_kernel<false, 2>)
                             : reinterpret_cast<const void*>(fp8_norm_kernel<false, 4>);
-  return launch_pdl(fn, (unsigned)(((long long)a.M + rpc - 1) / rpc), 32 * warps, warps * 2 * A * steps * 4, s, ptrs);
+  return launch_pdl(fn, (unsigned)(((long long)a.M + rpc - 1) / rpc), 32 * warps, warps * 2 * A * pl.steps * 4, s,
+                    ptrs);
 }
 
 }  // namespace svdq

@@ -425,6 +425,12 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
 
 }  // namespace
 
+bool fp8_pair_holds(const Fp8GemmArgs& a) {
+  const int tiles = ((a.M + 255) / 256) * ((a.N + BN - 1) / BN), pairs = a.num_sms / 2;
+  const long long blocks = (long long)((tiles + pairs - 1) / pairs) * ((a.K + 127) / 128);   // K blocks of a pair
+  return blocks >= kHoldBlocks;
+}
+
 cudaError_t launch_fp8_linear(const Fp8GemmArgs& a, cudaStream_t s) {
   int tokens, split;
   if (fp8_rows_plan(a, &tokens, &split)) return launch_fp8_rows(a, tokens, split, s);
@@ -450,8 +456,7 @@ cudaError_t launch_fp8_linear(const Fp8GemmArgs& a, cudaStream_t s) {
   p.wait_ns = a.wait_ns;
   const size_t smem = sizeof(Smem) + 1024;
   const int tiles = p.tiles_m * p.tiles_n, pairs = a.num_sms / 2;
-  const long long blocks = (long long)((tiles + pairs - 1) / pairs) * p.G;   // K blocks of a pair
-  auto kern = blocks >= kHoldBlocks ? gemm_fp8_kernel<true> : gemm_fp8_kernel<false>;
+  auto kern = fp8_pair_holds(a) ? gemm_fp8_kernel<true> : gemm_fp8_kernel<false>;
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

@@ -116,6 +116,12 @@ struct Fp8ActArgs {
   float eps;
 };
 constexpr int kFp8NormMaxK = 32768;
+// What the activation pass takes for its sizes: loads of a thread in flight
+// (without the norm: pieces of 256 columns a warp), warps of a row, steps of a row.
+struct Fp8ActPlan {
+  int loads, warps, steps;
+};
+Fp8ActPlan fp8_act_plan(int M, int K, bool norm, bool residual, int num_sms);
 cudaError_t launch_fp8_act(const Fp8ActArgs& a, int num_sms, cudaStream_t s);
 
 // W [K, N] -> codes [N, K], scales [ceil(N/128), ceil(K/128)]
@@ -138,6 +144,8 @@ cudaError_t launch_fp8_linear(const Fp8GemmArgs& a, cudaStream_t s);
 // few rows (gemm_fp8_rows.cu): whether that kernel is taken, and with which
 // token tile and split of K; launch_fp8_linear dispatches to it
 bool fp8_rows_plan(const Fp8GemmArgs& a, int* tokens, int* split);
+// many rows (gemm_fp8.cu): whether its long-run instance is taken
+bool fp8_pair_holds(const Fp8GemmArgs& a);
 cudaError_t launch_fp8_rows(const Fp8GemmArgs& a, int tokens, int split, cudaStream_t s);
 
 constexpr int kRopeMaxPairs = 512;

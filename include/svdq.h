@@ -380,6 +380,16 @@ svdq_status svdq_probe_wait_timeout(unsigned long long limit_ns, void* stream);
  * (SMs/2) * iters * 4 * 2*256*256*64 FLOP. 1 <= iters <= 2^20, 0 <= mode <= 4. */
 svdq_status svdq_probe_mma_peak(int iters, int mode, void* stream);
 
+/* Which kernels the 8-bit layer takes for its sizes on a device of `sms`
+ * multiprocessors (host only, for tests that every variant is reached):
+ * linear: plan[0] = tokens of a tile, plan[1] = parts of K (few rows: 16, 32,
+ *   64 or 128 tokens, 1 to 8 parts), or 256 and whether a run is long (many rows);
+ * act: plan[0] = loads of a thread in flight (without the norm pieces of 256
+ *   columns a warp), plan[1] = warps of a row.
+ * Sizes as svdq_fp8_linear, svdq_fp8_norm_quantize and svdq_fp8_quantize_act, M >= 1. */
+svdq_status svdq_probe_fp8_linear_plan(int M, int K, int N, int sms, int plan[2]);
+svdq_status svdq_probe_fp8_act_plan(int M, int K, int norm, int residual, int sms, int plan[2]);
+
 /* Test hook: pretend the device has compute capability major.minor (0, 0
  * restores the real query), to exercise SVDQ_ERR_UNSUPPORTED_ARCH. */
 void svdq_debug_force_arch(int major, int minor);

@@ -77,7 +77,7 @@ def test_few_rows(M, K, N, sure, out):
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
-@pytest.mark.parametrize("M,K,N,sure", [(300, 400, 4096, False), (600, 640, 2560, False), (1100, 2064, 4104, False),
+@pytest.mark.parametrize("M,K,N,sure", [(2560, 512, 4096, False), (4608, 640, 12288, False), (1100, 2064, 4104, False),
                                         (4608, 1152, 4096, False), (8192, 8192, 8192, True)])
 def test_many_rows(M, K, N, sure, out):
     """As many blocks of K as there are stages and fewer, tiles for some of the
