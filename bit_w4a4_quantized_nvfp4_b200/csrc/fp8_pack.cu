@@ -3,19 +3,13 @@
 // block: it finds the block's largest magnitude (a first pass over W), then
 // turns the block through shared memory so that both the reads (along N) and
 // the writes (along K) are contiguous. Not on a timed path.
-#include "device.cuh"
+#include "fp8.cuh"
 #include "kernels.h"
 
 namespace svdq {
 namespace {
 
 constexpr int kThreadsP = 256;
-
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 
 __global__ void __launch_bounds__(kThreadsP) fp8_pack_kernel(int K, int N, const float* __restrict__ W,
                                                              uint8_t* __restrict__ codes,
@@ -34,7 +28,7 @@ __global__ void __launch_bounds__(kThreadsP) fp8_pack_kernel(int K, int N, const
   __syncthreads();
   am = part[0];
   for (int i = 1; i < kThreadsP / 32; ++i) am = max_nan(am, part[i]);
-  const float scale = max_nan(am / 448.0f, 1.17549435e-38f);
+  const float scale = max_nan(am / 448.0f, kFp8MinScale);
   for (int i = threadIdx.x; i < 128 * 128; i += kThreadsP) {
     const int k = i >> 7, n = i & 127;
     if (k < nk && n < nn) tile[n][k] = (uint8_t)cvt_e4m3(W[(size_t)(k0 + k) * N + n0 + n] / scale);

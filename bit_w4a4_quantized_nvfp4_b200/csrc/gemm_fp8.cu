@@ -82,7 +82,7 @@ struct Params {
   const float* x_scales;
   const float* w_scales;
   const uint16_t* bias;
-  int M, N, K, G;
+  int M, N, G;
   int tiles_m, tiles_n;    // 256-row and 256-column tiles
   int out_f32;
   unsigned* err;
@@ -447,7 +447,7 @@ cudaError_t launch_fp8_linear(const Fp8GemmArgs& a, cudaStream_t s) {
   p.x_scales = a.x_scales;
   p.w_scales = a.w_scales;
   p.bias = a.bias;
-  p.M = a.M; p.N = a.N; p.K = a.K;
+  p.M = a.M; p.N = a.N;
   p.G = (a.K + 127) / 128;
   p.tiles_m = (a.M + 255) / 256;
   p.tiles_n = (a.N + BN - 1) / BN;

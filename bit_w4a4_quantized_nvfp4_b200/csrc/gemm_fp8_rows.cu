@@ -366,7 +366,8 @@ cudaError_t launch_rows_t(const Fp8GemmArgs& a, int split, cudaStream_t s) {
 }  // namespace
 
 // Of 148 SMs, those on which clusters of a size find room at one CTA an SM (a
-// cluster stays within a processing cluster of 16 to 20 SMs).
+// cluster stays within a processing cluster of 16 to 20 SMs). A device with
+// another number of SMs would have other figures: these are scaled, unmeasured.
 constexpr int kRoom[kMaxSplit + 1] = {0, 148, 148, 135, 132, 130, 132, 105, 120};
 
 // Up to 32 tokens the tile is as wide as they are and two CTAs fit on an SM; K is
