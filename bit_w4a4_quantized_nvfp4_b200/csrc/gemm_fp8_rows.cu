@@ -93,6 +93,7 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
   uint64_t* mma_done = acc_free + C::kBufs;
   uint64_t* joined = mma_done + 1;
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(joined + 1);
+  volatile uint32_t* left = tmem_ptr + 1;   // whether the producer or the MMA warp has given up
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)blockIdx.x % p.split, tn = (int)blockIdx.x / p.split;
@@ -106,6 +107,7 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
   const int groups = min(per / 4, (max(tv - rank * per, 0) + 3) / 4);   // this CTA's
 
   if (threadIdx.x == 0) {
+    *left = 0;
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -144,22 +146,21 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
   if (threadIdx.x == 0) launch_dependents();
   grid_dependency_wait();
 
+  int issued = 0;   // blocks (thread 0)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      int k = 0;
-      for (; k < nkb; ++k) {
-        const int s = k % S;
-        if (k >= S && !mbar_wait(&empty[s], ((k / S) - 1) & 1, p.wait_ns, p.err)) break;
+      for (; issued < nkb; ++issued) {
+        const int k = issued, s = k % S;
+        if (k >= S && !mbar_wait(&empty[s], ((k / S) - 1) & 1, p.wait_ns, p.err)) {
+          *left = 1;
+          break;
+        }
         uint8_t* st = stages + s * C::kStageBytes;
         mbar_expect_tx(&full[s], C::kStageBytes);
         tma_load_2d(st, &tm_w, &full[s], (kb0 + k) * 128, n0);
         tma_load_2d(st + C::kWBytes, &tm_x, &full[s], (kb0 + k) * 128, m0);
       }
-      // The copies issued land before the CTA can exit, whichever warp's wait ran
-      // out (the MMA warp may have left blocks that it never waited for; where
-      // none ran out they have landed by now)
-      for (int j = max(0, k - S); j < k; ++j) (void)mbar_wait(&full[j % S], (j / S) & 1, kLandNs, nullptr);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -175,8 +176,10 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
       const bool rf = mbar_try_wait(&acc_free[b], bph);
       const bool rs = mbar_try_wait(&full[s], sph);
       if (!__all_sync(0xffffffffu, rs && rf) && !(warp_wait(&full[s], sph, p.wait_ns, p.err) &&
-                                                  warp_wait(&acc_free[b], bph, p.wait_ns, p.err)))
+                                                  warp_wait(&acc_free[b], bph, p.wait_ns, p.err))) {
+        if (lane == 0) *left = 1;
         break;
+      }
       tc_fence_after();
       const uint64_t da = a0 + (uint64_t)(s * (C::kStageBytes >> 4)), db = b0 + (uint64_t)(s * (C::kStageBytes >> 4));
       if (elect_one()) {
@@ -317,6 +320,10 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
+  // Where the producer's wait ran out, or the MMA warp's, which then leaves
+  // blocks that it never waited for, the copies issued land before the CTA exits
+  if (threadIdx.x == 0 && *left)
+    for (int j = max(0, issued - S); j < issued; ++j) (void)mbar_wait(&full[j % S], (j / S) & 1, kLandNs, nullptr);
 }
 
 template <int T>
