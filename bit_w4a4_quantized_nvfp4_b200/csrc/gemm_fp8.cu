@@ -76,6 +76,7 @@ struct Smem {
   uint64_t acc_full[4], acc_free[4], mma_done;
   uint64_t out_ready[kDrainWarps], out_free;
   uint32_t tmem_base;
+  uint32_t left;   // whether the producer or an issuer has given up (leader)
 };
 
 struct Params {
@@ -106,6 +107,9 @@ __device__ __forceinline__ void tile_at(int t, const Params& p, int& tm, int& tn
   tn = r / rows;
 }
 
+// The leader's producer and issuers at the end of their loops.
+__device__ __forceinline__ void issuers_done() { asm volatile("bar.sync 1, 96;" ::: "memory"); }
+
 // kHold: the early test of the next block's barrier may hold the warp until the
 // barrier turns (try_wait) or only looks (test_wait). Looking is faster while a
 // pair has few K blocks to do (21.7 us against 23.5 at 1024 x 4096 x 4096, 59.7
@@ -127,6 +131,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
   const int num_tiles = p.tiles_m * p.tiles_n;
 
   if (threadIdx.x == 0) {
+    sm.left = 0;
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sm.full[s], 1);
       mbar_init(&sm.empty[s], 2);   // both issuers
@@ -161,8 +166,8 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     regs_dec<kOtherRegs>();
     if (warp == 0) {
       // ---------------------------------------------------------- producer
+      uint32_t it = 0;
       if (lane == 0) {
-        uint32_t it = 0;
         bool ok = true;
         for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
           int tm, tn;
@@ -180,15 +185,23 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
             tma_load_2d_pair(st + kABytes + kBBytes / 2, &tm_b, fb, kb * BK, col0 + UN);
           }
         }
-        // The copies issued land before the pair exits, whichever warp's wait ran
-        // out (the issuers may have left blocks that they never waited for). Both
-        // CTAs' count on the leader's barriers; a CTA that has stopped early
-        // leaves blocks without its half, which never turn them.
-        if (leader) {
+        if (!ok) {
+          sm.left = 1;
+          if (!leader) let_copies_land();   // (they count on the leader's barriers)
+        }
+      }
+      __syncwarp();
+      // Where the leader's producer or an issuer gave up (it then leaves blocks
+      // that it never waited for), the copies issued land before the pair exits.
+      // Both CTAs' count on the leader's barriers; a block that one of them did
+      // not issue never turns its barrier, so copies past it have their time.
+      if (leader) {
+        issuers_done();
+        if (lane == 0 && sm.left) {
           for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
             if (!mbar_wait(&sm.full[j % kStages], (j / kStages) & 1, kLandNs, nullptr)) break;
+          let_copies_land();
         }
-        if (!ok) let_copies_land();
       }
     } else if ((warp == 1 || warp == 3) && leader) {
       // ---------------------------------------------------------- MMA issuers
@@ -228,10 +241,12 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           }
         }
       }
+      if (!ok && lane == 0) sm.left = 1;
       // every MMA issued has completed before tensor memory is freed
       if (elect_one()) tc_commit_pair(&sm.mma_done, 0x1);
       __syncwarp();
       (void)warp_wait(&sm.mma_done, 0, kLandNs, p.err);
+      issuers_done();
     } else if (warp == 2 && !p.out_f32) {
       // ---------------------------------------------------------- output copies
       uint32_t tl = 0;
