@@ -5,9 +5,9 @@
 //   per 128 columns: scale = max(max|v| / 448, 2^-126), code = e4m3(v / scale)
 // Bound by HBM: 3 bytes an element, 7 with a residual. Measured from HBM
 // (launches in a row over three sets of inputs): norm + residual 4608 x 4096
-// 20.6 us, 6.4 TB/s, 0.99 of the measured copy rate (20.4 us at that rate); 8192
-// x 8192 67.8 us; norm alone 4608 x 12288 29.5 us, 0.89; without the norm 4608 x
-// 12288 28.2 us, 0.94. What is left of the norm's is the columns' arithmetic,
+// 21.1 us, 6.3 TB/s, 0.97 of the measured copy rate (20.4 us at that rate); 8192
+// x 8192 67.9 us; norm alone 4608 x 12288 29.3 us, 0.90; without the norm 4608 x
+// 12288 28.3 us, 0.93. What is left of the norm's is the columns' arithmetic,
 // some ten instructions each.
 //
 // A load is 8 consecutive columns (16 bytes of bf16); a block of 128 is 16 of
@@ -324,8 +324,8 @@ Fp8ActPlan fp8_act_plan(int M, int K, bool norm, bool residual, int num_sms) {
   // barrier, the least work beside the columns), more for fewer rows, but no
   // more than the row has columns for. With a residual a thread has at most four
   // vectors, unless more warps would leave lanes idle: memory takes few long
-  // streams better than many (8192 x 8192 68.4 us, 71.4 with eight, 76.6 with a
-  // row a warp; 4608 x 4096 20.9, 21.3, 23.2; 1200 x 8192 12.4 against 15.0; but
+  // streams better than many (in turn on one box: 8192 x 8192 68.4 us, 71.4 with
+  // eight, 76.6 with a row a warp; 4608 x 4096 20.9, 21.3, 23.2; 1200 x 8192 12.4 against 15.0; but
   // 1024 x 8192 10.8 against 10.2). Without one it is the other way round (4608
   // x 12288 29.7, 37.1 with eight).
   const int nv = K / 8;

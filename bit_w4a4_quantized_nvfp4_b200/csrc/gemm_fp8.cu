@@ -1,5 +1,5 @@
 // The 8-bit GEMM (svdq_fp8_linear) for many rows:
-//   y[m,n] = sum_g sx[g,m] sw[n/128,g] sum_{k in g} qx[m,k] qw[n,k] + bias[n]
+//   y[m,n] = sum_g (sx[g,m] sw[n/128,g]) sum_{k in g} qx[m,k] qw[n,k] + bias[n]
 //
 // A block's product is one accumulator of the tensor cores; the scales are
 // fp32 and differ from block to block of 128 along K, so a block's sums leave
@@ -36,15 +36,15 @@
 //     products and two accumulators for both halves: 478 against 469).
 //   - A tile's end is short: the drain stages its columns and goes on, warp 2
 //     issues the copies (a warp waits 1000 cycles to issue its own), and the
-//     next tile's scales are loaded ahead (4608 x 1024 x 9216 with bias 62 us,
-//     58 so). Output straight from the registers, 32 bytes a store, was slower
+//     next tile's scales are loaded ahead (4608 x 1024 x 9216 with bias 62 us, 58
+//     so, in turn on one box). Output straight from the registers, 32 bytes a store, was slower
 //     than the staging (522 us against 510 at 8192^3): a thread's stores are
 //     rows apart.
-// Measured: 8192^3 450 us (2.44 PFLOP/s; the measured bf16 rate is 1.65 in
-// bursts, so 0.74 of twice that), 4608 x 4096 x 12288 203 us (2.28), 1024 x 4096 x
-// 4096 20.3 us. The large ones run into the 1000 W limit: the SMs go down to 1.35
-// GHz, and back to back for a second 8192^3 takes 530 us (2.07 PFLOP/s, 1.5 times
-// the bf16 rate under the same limit). A copy of an earlier version (463 us)
+// Measured: 8192^3 443 to 465 us by box (2.36 to 2.48 PFLOP/s; the measured bf16
+// rate is 1.65 in bursts, so 0.71 to 0.75 of twice that), 4608 x 4096 x 12288 198
+// to 207 us (2.24 to 2.34), 1024 x 4096 x 4096 21.4 us. The large ones run into the
+// 1000 W limit: the SMs go down to 1.35 GHz, and back to back for a second 8192^3
+// takes 523 us (2.10 PFLOP/s, 1.5 times the bf16 rate under the same limit). A copy of an earlier version (463 us)
 // without the drain's arithmetic and loads took 425 us at the same power: what
 // bounds it is energy, the operands' way to the SMs and the products themselves.
 #include "fp8.cuh"
@@ -112,10 +112,11 @@ __device__ __forceinline__ void issuers_done() { asm volatile("bar.sync 1, 96;" 
 
 // kHold: the early test of the next block's barrier may hold the warp until the
 // barrier turns (try_wait) or only looks (test_wait). Looking is faster while a
-// pair has few K blocks to do (21.7 us against 23.5 at 1024 x 4096 x 4096, 59.7
-// against 62.3 at 4608 x 1024 x 9216); in long runs holding is (530 us against
-// 538 at 8192^3, 240 against 243 at 4608 x 4096 x 12288): the halves' drains then
-// fall into step. At 2048 x 4096 x 12288, 192 blocks a pair, both take 115 us.
+// pair has few K blocks to do (21.6 us against 24.7 at 1024 x 4096 x 4096, 53.9
+// against 57.0 at 4608 x 1024 x 9216 with bias); in long runs holding is (454 us
+// against 469 at 8192^3, 202 against 207 at 4608 x 4096 x 12288): the halves'
+// drains then fall into step. At 2048 x 4096 x 12288, 192 blocks a pair, holding
+// takes 98.2 us, looking 99.5.
 constexpr int kHoldBlocks = 256;
 
 template <bool kHold>

@@ -294,10 +294,12 @@ svdq_status svdq_fp8_norm_quantize(int M, int K, const uint16_t* x, long long ld
 svdq_status svdq_fp8_pack_weight(int K, int N, const float* W, uint8_t* codes, float* scales, void* stream);
 
 /* svdq_fp8_linear — the 8-bit GEMM:
- *   y[m,n] = sum_g sx[g,m] sw[n/128,g] sum_{k in g} qx[m,k] qw[n,k] + bias[n]
+ *   y[m,n] = sum_g (sx[g,m] sw[n/128,g]) sum_{k in g} qx[m,k] qw[n,k] + bias[n]
  * The products of a block are summed in fp32 by the tensor cores, the blocks
  * in fp32; one rounding at the end. The order of the sums depends on the
- * sizes alone, so a call repeated gives the same bits.
+ * sizes alone, so a call repeated gives the same bits. The two scales' product
+ * is formed first, in fp32: where it leaves fp32's range (below 2^-126 it loses
+ * bits) so do the sums.
  * In:  codes and scales of both operands; bias bf16 [N] or NULL.
  * Out: y [M, N], bf16 (SVDQ_OUT_BF16) or fp32 (SVDQ_OUT_F32), overlapping no
  *      input (SVDQ_ERR_INVALID_ARG); other output modes give
