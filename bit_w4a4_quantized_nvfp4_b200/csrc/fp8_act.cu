@@ -217,8 +217,9 @@ __global__ void __launch_bounds__(512, 2) fp8_norm_kernel(const Fp8ActArgs a, in
     if (live && g * 16 < nv) a.scales[(size_t)g * a.M + m] = scale_of(top);
     // Past fp32; or zeros that may be products r w below 2^-150, which count
     // where 1 / rms brings them past the smallest code of the smallest scale,
-    // 2^-136 (so not in a row of zeros with an eps of 2^-26 or more)
-    odd = odd || top > 0x1.fffffep127f || (live && g * 16 < nv && am_w[l] == 0.f && inv > 0x1p13f);
+    // 2^-136 (with an eps of 2^-27 or more never; at 1e-12 a batch of nothing but
+    // zeros takes 25.7 us at 4608 x 4096, 11.3 at 1e-6)
+    odd = odd || top > 0x1.fffffep127f || (live && g * 16 < nv && am_w[l] == 0.f && inv > 0x1.8p13f);
   }
   if (__any_sync(0xffffffffu, odd || least * inv * (1.0f / 448.0f) < kFp8MinScale || inv > 0x1p100f)) {
     // the smallest scale, NaN, infinities, values, products r w or a factor
@@ -325,9 +326,9 @@ Fp8ActPlan fp8_act_plan(int M, int K, bool norm, bool residual, int num_sms) {
   // more than the row has columns for. With a residual a thread has at most four
   // vectors, unless more warps would leave lanes idle: memory takes few long
   // streams better than many (in turn on one box: 8192 x 8192 68.4 us, 71.4 with
-  // eight, 76.6 with a row a warp; 4608 x 4096 20.9, 21.3, 23.2; 1200 x 8192 12.4 against 15.0; but
-  // 1024 x 8192 10.8 against 10.2). Without one it is the other way round (4608
-  // x 12288 29.7, 37.1 with eight).
+  // eight, 76.6 with a row a warp; 4608 x 4096 20.9, 21.3, 23.2; 1200 x 8192 12.4
+  // against 15.0; but 1024 x 8192 10.8 against 10.2). Without one it is the other
+  // way round (4608 x 12288 29.7, 37.1 with eight).
   const int nv = K / 8;
   auto lanes = [nv](int w) { return (nv + 64 * w - 1) / (64 * w) * 64 * w; };   // steps come in twos
   int wpr = 1;

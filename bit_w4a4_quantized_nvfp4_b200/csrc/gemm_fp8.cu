@@ -37,16 +37,17 @@
 //   - A tile's end is short: the drain stages its columns and goes on, warp 2
 //     issues the copies (a warp waits 1000 cycles to issue its own), and the
 //     next tile's scales are loaded ahead (4608 x 1024 x 9216 with bias 62 us, 58
-//     so, in turn on one box). Output straight from the registers, 32 bytes a store, was slower
-//     than the staging (522 us against 510 at 8192^3): a thread's stores are
-//     rows apart.
+//     so, in turn on one box). Output straight from the registers, 32 bytes a
+//     store, was slower than the staging (522 us against 510 at 8192^3): a
+//     thread's stores are rows apart.
 // Measured: 8192^3 443 to 465 us by box (2.36 to 2.48 PFLOP/s; the measured bf16
 // rate is 1.65 in bursts, so 0.71 to 0.75 of twice that), 4608 x 4096 x 12288 198
 // to 207 us (2.24 to 2.34), 1024 x 4096 x 4096 21.4 us. The large ones run into the
 // 1000 W limit: the SMs go down to 1.35 GHz, and back to back for a second 8192^3
-// takes 523 us (2.10 PFLOP/s, 1.5 times the bf16 rate under the same limit). A copy of an earlier version (463 us)
-// without the drain's arithmetic and loads took 425 us at the same power: what
-// bounds it is energy, the operands' way to the SMs and the products themselves.
+// takes 523 us (2.10 PFLOP/s, 1.5 times the bf16 rate under the same limit). A
+// copy of an earlier version (463 us) without the drain's arithmetic and loads
+// took 425 us at the same power: what bounds it is energy, the operands' way to
+// the SMs and the products themselves.
 #include "fp8.cuh"
 #include "kernels.h"
 
@@ -442,9 +443,8 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
 }  // namespace
 
 bool fp8_pair_holds(const Fp8GemmArgs& a) {
-  const int tiles = ((a.M + 255) / 256) * ((a.N + BN - 1) / BN), pairs = a.num_sms / 2;
-  const long long blocks = (long long)((tiles + pairs - 1) / pairs) * ((a.K + 127) / 128);   // K blocks of a pair
-  return blocks >= kHoldBlocks;
+  const long long tiles = (long long)((a.M + 255) / 256) * ((a.N + BN - 1) / BN), pairs = a.num_sms / 2;
+  return (tiles + pairs - 1) / pairs * ((a.K + 127) / 128) >= kHoldBlocks;   // K blocks of a pair
 }
 
 cudaError_t launch_fp8_linear(const Fp8GemmArgs& a, cudaStream_t s) {

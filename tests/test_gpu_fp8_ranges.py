@@ -134,3 +134,30 @@ def test_products_with_the_weight_below_fp32(M, K, residual):
     plain.check_codes(qa.codes, qa.scales, v, NORM_DELTA)
     if K > 256:
         assert (qa.codes[2, :256].float() == 0).all() and (qa.scales[:2, 2] == plain.MIN_SCALE).all()
+
+
+def test_rows_of_zeros_among_small_ones():
+    """A padded batch at an eps that counts for nothing else: zeros stay zeros
+    at the smallest scale beside rows of any size."""
+    x = _acts(300, 400, 9)
+    x[100:200] = 0.0
+    x[200:] = (x[200:].float() * 1e-7).to(torch.bfloat16)
+    x[250, 128:256] = 0.0
+    w = torch.ones(400, dtype=torch.bfloat16, device="cuda")
+    for eps in (1e-12, 1e-30):
+        qa = _norm(x, w, eps, False)
+        v, _ = plain.norm64(x, w, eps)
+        plain.check_codes(qa.codes, qa.scales, v, NORM_DELTA)
+        assert (qa.codes[100:200].float() == 0).all() and (qa.scales[:, 100:200] == plain.MIN_SCALE).all()
+
+
+@pytest.mark.parametrize("residual", [False, True])
+def test_products_below_fp32_with_an_eps(residual):
+    """As above where eps alone sets the norm and the row's squares vanish
+    beside it: v = 2^-84 * 1e6 * 2^-70, some 2^-134, a code of some 2^-8."""
+    x = torch.full((40, 400), 2.0 ** -84, dtype=torch.bfloat16, device="cuda")
+    w = torch.full((400,), 2.0 ** -70, dtype=torch.bfloat16, device="cuda")
+    qa = _norm(x, w, 1e-12, residual)
+    v, _ = plain.norm64(x, w, 1e-12)
+    plain.check_codes(qa.codes, qa.scales, v, NORM_DELTA)
+    assert (qa.codes.float() > 0).all()
