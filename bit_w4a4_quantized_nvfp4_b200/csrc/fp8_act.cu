@@ -325,7 +325,7 @@ Fp8ActPlan fp8_act_plan(int M, int K, bool norm, bool residual, int num_sms) {
   // barrier, the least work beside the columns), more for fewer rows, but no
   // more than the row has columns for. With a residual a thread has at most four
   // vectors, unless more warps would leave lanes idle: memory takes few long
-  // streams better than many (in turn on one box: 8192 x 8192 68.4 us, 71.4 with
+  // streams better than many (in turn on one card: 8192 x 8192 68.4 us, 71.4 with
   // eight, 76.6 with a row a warp; 4608 x 4096 20.9, 21.3, 23.2; 1200 x 8192 12.4
   // against 15.0; but 1024 x 8192 10.8 against 10.2). Without one it is the other
   // way round (4608 x 12288 29.7, 37.1 with eight).

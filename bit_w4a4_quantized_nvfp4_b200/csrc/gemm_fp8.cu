@@ -37,10 +37,10 @@
 //   - A tile's end is short: the drain stages its columns and goes on, warp 2
 //     issues the copies (a warp waits 1000 cycles to issue its own), and the
 //     next tile's scales are loaded ahead (4608 x 1024 x 9216 with bias 62 us, 58
-//     so, in turn on one box). Output straight from the registers, 32 bytes a
+//     so, in turn on one card). Output straight from the registers, 32 bytes a
 //     store, was slower than the staging (522 us against 510 at 8192^3): a
 //     thread's stores are rows apart.
-// Measured: 8192^3 443 to 465 us by box (2.36 to 2.48 PFLOP/s; the measured bf16
+// Measured: 8192^3 443 to 465 us by card (2.36 to 2.48 PFLOP/s; the measured bf16
 // rate is 1.65 in bursts, so 0.71 to 0.75 of twice that), 4608 x 4096 x 12288 198
 // to 207 us (2.24 to 2.34), 1024 x 4096 x 4096 21.4 us. The large ones run into the
 // 1000 W limit: the SMs go down to 1.35 GHz, and back to back for a second 8192^3

@@ -389,7 +389,7 @@ constexpr int kRoom[kMaxSplit + 1] = {0, 148, 148, 135, 132, 130, 132, 105, 120}
 // Measured at N = 4096 with 8, 32 and 64 blocks: T = 64 5.9, 12.3, 20.7 us
 // (a = 3.8, c = 0.265), T = 128 8.0, 15.6, 26.4 (5.4, 0.33), the pair kernel
 // 10.1, 20.3, 33.4; three waves of it at 8 and 32 blocks 19.3, 47.2. So M = 512,
-// N = K = 4096 comes here (in turn on one box 16.6 us against 20.3), M = 512 with
+// N = K = 4096 comes here (in turn on one card 16.6 us against 20.3), M = 512 with
 // N = 12288 does not (33.6 on the pair kernel, three waves here). Splits of any
 // number help here too (64 x 4096 x 5120: by 3 8.1 us, by 2 9.9; 77 x 2064 x 1000:
 // by 6 4.9, by 4 5.2).
