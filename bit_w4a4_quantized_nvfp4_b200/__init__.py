@@ -475,10 +475,12 @@ def _blocks(n: int) -> int:
     return (n + 127) // 128
 
 
-def _sizes(a: int, b: int, c: int = 0) -> None:
-    """Sizes go to the library as C ints, which ctypes would wrap."""
-    if a > 0x7FFFFFFF or b > 0x7FFFFFFF or c > 0x7FFFFFFF:
-        raise ValueError(f"size {max(a, b, c)}: 2^31 - 1 is the largest")
+# Sizes go to the library as C ints, which ctypes would wrap.
+_MOST = 0x7FFFFFFF
+
+
+def _too_large(*sizes: int) -> None:
+    raise ValueError(f"size {max(sizes)}: 2^31 - 1 is the largest")
 
 
 def _rows(t: torch.Tensor, name: str):
@@ -489,7 +491,8 @@ def _rows(t: torch.Tensor, name: str):
     if t.dtype is not _BF16 or t.dim() != 2:
         raise ValueError(f"{name}: expected bfloat16 [M, K]")
     M, K = t.shape
-    _sizes(M, K)
+    if M > _MOST or K > _MOST:
+        _too_large(M, K)
     s0, s1 = t.stride()
     if s1 != 1 and K > 1:
         raise ValueError(f"{name}: expected unit stride along the columns")
@@ -599,7 +602,8 @@ def fp8_pack_weight(W: torch.Tensor, stream=None, out: Optional[Fp8Weight] = Non
     """svdq_fp8_pack_weight: W fp32 [K, N] -> codes, scales (into ``out``'s buffers when given)."""
     _need(W.dim() == 2 and W.dtype == torch.float32, "W: expected float32 [K, N]")
     K, N = W.shape
-    _sizes(K, N)
+    if K > _MOST or N > _MOST:
+        _too_large(K, N)
     dev = _current(W)
     if out is None:
         out = Fp8Weight(K, N, _new(N, K, _F8, W.device, stream),
@@ -621,7 +625,8 @@ def fp8_linear(qa: Fp8Act, w: Fp8Weight, bias: Optional[torch.Tensor] = None, ou
     if K != w.K:
         raise ValueError(f"activations have K = {K}, the packed weight K = {w.K}")
     _need(out_dtype == "bf16" or out_dtype == "f32", "out_dtype {!r}", out_dtype)
-    _sizes(M, K, N)
+    if M > _MOST or K > _MOST or N > _MOST:
+        _too_large(M, K, N)
     G = (K + 127) // 128
     xc, xs, wc, ws = qa.codes, qa.scales, w.codes, w.scales
     _is(xc, _F8, (M, K), "qa.codes")
@@ -712,7 +717,8 @@ def _rope_inputs(positions: torch.Tensor, freqs: RopeFreqs):
     if f.dtype is not torch.float64 or f.dim() != 1:
         raise ValueError("freqs.freq: expected float64 [pairs]")
     pairs = f.shape[0]
-    _sizes(M, axes, pairs)
+    if M > _MOST or axes > _MOST or pairs > _MOST:
+        _too_large(M, axes, pairs)
     if axis is not None:
         _is(axis, torch.int32, (pairs,), "freqs.axis")
     dev = _current(positions)
